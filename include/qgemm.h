@@ -33,6 +33,13 @@
  *                   fp16 activations. Canonical codes are u8
  *                   [N][K] as for QGEMM_INT8_B0, pairs [N][K/b][2].
  *
+ *   QGEMM_MXFP4     microscaled 4-bit floats (OCP Microscaling Formats v1.0,
+ *                   MXFP4): E2M1 codes and one E8M0 scale (a power of two) per
+ *                   32 K-elements; fp16 activations. K % 64 == 0.
+ *   QGEMM_MXFP4_A4  MXFP4 weights as above, and every row of A quantised to
+ *                   MXFP4 on the fly: both operands enter the matrix cores as
+ *                   4-bit codes with their scales, fp32 accumulation.
+ *
  * Format ids 0-3 equal the page's mode numbers. For every format but F32, A
  * is fp16; C is fp32 (or fp16 through qgemm_run_ex).
  *
@@ -47,7 +54,12 @@
  *   - W4A8, INT4_B0: q as INT4_B64 with one block over all of K; pairs
  *               float [N][1][2].
  *   - INT4_BLOCK(b): q as INT4_B64; pairs float [N][K/b][2].
- * Codes are unsigned: q in [0, 2^bits - 1].
+ *   - MXFP4, MXFP4_A4: q as INT4_B64; scales uint8 [N][K/32] instead of
+ *               pairs, so the functions that take `float *pairs` (and
+ *               qgemm_canonical_size) answer ERR_FORMAT for them and the
+ *               qgemm_mx_* functions stand in their place.
+ * Codes are unsigned: q in [0, 2^bits - 1]. An MXFP4 code is a sign bit (8)
+ * over the E2M1 magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (0..7).
  *
  * Packed (device) layouts are opaque and owned by this library: they are
  * produced by qgemm_pack_weights on the host, copied to device memory by the
@@ -89,6 +101,8 @@ typedef enum qgemm_format {
     QGEMM_W4A8 = 3,
     QGEMM_F16 = 4,
     QGEMM_INT4_B0 = 5,
+    QGEMM_MXFP4 = 6,
+    QGEMM_MXFP4_A4 = 8,
     QGEMM_INT4_BLOCK_BASE = 0x10000,  /* + b: see QGEMM_INT4_BLOCK */
     QGEMM_INT8_BLOCK_BASE = 0x2000000 /* + b: see QGEMM_INT8_BLOCK */
 } qgemm_format;
@@ -105,9 +119,9 @@ typedef enum qgemm_status {
     QGEMM_OK = 0,
     QGEMM_ERR_NULL = 1,     /* a required pointer is NULL                     */
     QGEMM_ERR_SHAPE = 2,    /* a shape is negative, too large, or violates the
-                               format's block rule (INT4_B64: K % 64 == 0;
+                               format's block rule (INT4_B64, MXFP4: K % 64 == 0;
                                INT4/W4A8: K even; quantised formats: K > 0)   */
-    QGEMM_ERR_FORMAT = 3,   /* unknown format, or an operation the format does
+    QGEMM_ERR_FORMAT = 3,   /* unknown format or type, or an operation the format does
                                not have (e.g. quantising to F32)              */
     QGEMM_ERR_ALIGN = 4,    /* a device pointer is not 16-byte aligned        */
     QGEMM_ERR_NOMEM = 5,    /* the library could not allocate its scratch     */
@@ -162,7 +176,8 @@ qgemm_status qgemm_quantize_weights(int K, int N, qgemm_format f,
  * NaN or infinite weight before it runs, so instead of ERR_VALUE the block
  * (the channel, for the per-channel formats) that holds one gets NaN offset
  * and scale and zero codes.
- * Errors: ERR_FORMAT (F32, F16, unknown, and INT4_BLOCK(b) / INT8_BLOCK(b)
+ * Errors: ERR_FORMAT (F32, F16, the MXFP4 formats (qgemm_mx_quantize_device),
+ * unknown, and INT4_BLOCK(b) / INT8_BLOCK(b)
  * with b other than 16, 32 or a multiple of 64: blocks that straddle the
  * quantiser's 64-element steps; quantise those with qgemm_quantize_weights),
  * ERR_SHAPE, ERR_NULL, ERR_ALIGN (a pointer not 16-byte aligned), ERR_DEVICE,
@@ -176,7 +191,8 @@ qgemm_status qgemm_quantize_weights_device(int K, int N, qgemm_format f, const f
  * codes and pairs go straight into the packed layouts qgemm_run reads (Bq
  * and scales of qgemm_packed_size's w_bytes / s_bytes, every byte written,
  * padding as zeros), byte-identical to qgemm_pack_weights of the canonical
- * result. Same arguments, errors and non-finite handling.
+ * result. Same arguments, errors and non-finite handling; the MXFP4 formats are
+ * taken here too (by the rules and the packed layout given with qgemm_mx_*).
  */
 qgemm_status qgemm_quantize_pack_device(int K, int N, qgemm_format f, const float *W,
                                         void *Bq, void *scales, void *stream);
@@ -220,7 +236,8 @@ qgemm_status qgemm_unpack_weights(int K, int N, qgemm_format f,
  * Device scratch qgemm_run_ws may need for this shape; a function of
  * (M, K, N, f) alone. It holds, in order: for W4A8 the quantised
  * activations (int8 [M][K rounded up to 128]), the row scales (float [M])
- * and the row sums of the quantised activations (int32 [M]); then, when the
+ * and the row sums of the quantised activations (int32 [M]); for MXFP4_A4 the
+ * activation codes and scales (K rounded up to 256); then, when the
  * shape leaves too few output tiles (or, for the Int4 and W4A8 GEMVs, too
  * few 32-channel tiles) to fill the GPU and the kernel therefore splits K into S
  * slices, S partial products ([S][M][N], float; int32 for W4A8) that a
@@ -376,6 +393,150 @@ qgemm_status qgemm_w4a8_debug(int M, int K, int N, const void *A,
  * runs, never the result beyond rounding.
  */
 int qgemm_set_gemv_max_m(int max_m);
+
+/* ===========================================================================
+ * Microscaled 4-bit floats (MXFP4)
+ *
+ * A row of K elements (K % 32 == 0) is held as K/2 code bytes (two E2M1 codes
+ * a byte, low nibble first) and K/32 scale bytes. Block j (elements 32 j ..
+ * 32 j + 31) with largest magnitude m:
+ *   e = clamp(floor(log2 m) - 2, -127, 127), scale byte e + 127;
+ *   code = sign | nearest E2M1 magnitude of |x| 2^-e, ties to the even code,
+ *          at most 6 (|x| 2^-e is below 8, so the largest element of a block
+ *          may lose up to a quarter: the format's own rule).
+ * A block of zeros has scale byte 0 and keeps its signs; a block that holds a
+ * NaN or an infinity has scale byte 255 (NaN) and zero codes. The value of a
+ * code is magnitude x 2^(byte - 127), and NaN where the byte is 255.
+ * ======================================================================== */
+typedef enum qgemm_type {
+    QGEMM_TYPE_F32 = 0,
+    QGEMM_TYPE_F16 = 1,
+    QGEMM_TYPE_BF16 = 2
+} qgemm_type;
+
+/*
+ * Device quantiser of R rows of K elements: activations, or weights in their
+ * canonical layout.
+ *   X       device, element type t, row r at X + r * ldx (ldx >= K, in
+ *           elements; for R > 1 a row must start 16-byte aligned).
+ *   q       device uint8 [R][K/2];  scales  device uint8 [R][K/32].
+ * Enqueued on `stream`. R == 0 or K == 0 is a no-op.
+ * Errors: ERR_FORMAT (unknown type), ERR_SHAPE (K % 32 != 0, ldx < K, a
+ * negative or too large size), ERR_NULL, ERR_ALIGN (a pointer or a row of X
+ * not 16-byte aligned), ERR_DEVICE, ERR_LAUNCH.
+ */
+qgemm_status qgemm_mx_quantize_device(int R, int K, int t, const void *X, long long ldx, uint8_t *q,
+                                      uint8_t *scales, void *stream);
+
+/*
+ * The inverse: the values of R rows of codes, in type t (rounded to nearest
+ * even where the type cannot hold them), row r at Y + r * ldy. Elements
+ * between K and ldy are left as they were. Arguments and errors as
+ * qgemm_mx_quantize_device.
+ */
+qgemm_status qgemm_mx_dequantize_device(int R, int K, const uint8_t *q, const uint8_t *scales, int t,
+                                        void *Y, long long ldy, void *stream);
+
+/*
+ * Host quantiser: float X [R][K] (host) to codes and scales (host), the same
+ * rules bit for bit. Errors: ERR_SHAPE, ERR_NULL, ERR_VALUE (a NaN or an
+ * infinity; nothing useful is written then).
+ */
+qgemm_status qgemm_mx_quantize(int R, int K, const float *X, uint8_t *q, uint8_t *scales);
+
+/*
+ * Canonical codes [N][K/2] and scales [N][K/32] -> the packed layout qgemm_run
+ * reads (qgemm_packed_size of QGEMM_MXFP4 bytes; both MXFP4 formats share it).
+ * Pure permutation plus zero padding.
+ * qgemm_mx_pack works on host buffers; qgemm_mx_pack_device on device buffers,
+ * for E weights at once: weight e at q + e * N * K/2, scales + e * N * K/32,
+ * packed to w_packed + e * w_bytes, s_packed + e * s_bytes (the layout
+ * qgemm_run_grouped reads), enqueued on `stream`. (qgemm_quantize_pack_device
+ * goes from float weights to the packed layout in one step.)
+ * Errors: ERR_SHAPE, ERR_NULL; ERR_SIZE (host); ERR_ALIGN, ERR_DEVICE,
+ * ERR_LAUNCH (device).
+ */
+qgemm_status qgemm_mx_pack(int K, int N, const uint8_t *q, const uint8_t *scales, void *w_packed,
+                           size_t w_bytes, void *s_packed, size_t s_bytes);
+qgemm_status qgemm_mx_pack_device(int K, int N, int E, const uint8_t *q, const uint8_t *scales,
+                                  void *w_packed, void *s_packed, void *stream);
+
+/* ===========================================================================
+ * Mixture of experts: products grouped by expert
+ *
+ * T tokens choose topk experts each. A choice (t, j) whose id lies in [0, E)
+ * gets a slot; the slots of one expert are consecutive, experts ascending,
+ * choices in (t, j) order within an expert. Choices of any other id (an
+ * expert on another GPU, a dropped or padded token) have no slot.
+ *   qgemm_group_plan      the choices' ids -> that layout;
+ *   qgemm_run_grouped     one product per slot against its expert's weight;
+ *   qgemm_group_combine   every token's weighted sum over its slots.
+ * ======================================================================== */
+#define QGEMM_MAX_EXPERTS 1024
+
+/*
+ *   ids      device [T][topk], int64 if ids64 is nonzero, else int32.
+ *   offsets  device int32 [E + 1]: expert e owns slots [offsets[e],
+ *            offsets[e + 1]); offsets[0] = 0.
+ *   rows     device int32 [T * topk]: rows[s] = the token of slot s; behind
+ *            the last slot, the tokens of the choices without one, in order.
+ *   slots    device int32 [T][topk]: the slot of a choice, -1 without one.
+ * All outputs are fully written (T == 0 or topk == 0: offsets, all zero).
+ * workspace: device scratch of qgemm_group_plan_size() bytes, 16-byte aligned;
+ * with NULL and 0 any that is needed is allocated stream-ordered. Calls that
+ * share one must be ordered. Deterministic.
+ * Errors: ERR_SHAPE (E outside 1..QGEMM_MAX_EXPERTS, T * topk above 2^26, a
+ * negative size), ERR_NULL, ERR_ALIGN, ERR_SIZE, ERR_DEVICE, ERR_NOMEM,
+ * ERR_LAUNCH.
+ */
+qgemm_status qgemm_group_plan_size(int T, int topk, int E, size_t *bytes);
+qgemm_status qgemm_group_plan(int T, int topk, int E, const void *ids, int ids64, int32_t *offsets,
+                              int32_t *rows, int32_t *slots, void *workspace, size_t ws_bytes,
+                              void *stream);
+
+/*
+ * For every expert e and slot s in [offsets[e], offsets[e + 1]):
+ *   C[s] = act(A[rows[s]] x deq(B_e) + bias[e] + residual[s])
+ *   S         rows of C (the most slots there can be). Rows of C that no
+ *             expert owns are left as they were.
+ *   f         QGEMM_MXFP4 or QGEMM_MXFP4_A4.
+ *   A         device fp16 [a_rows][K].
+ *   rows      device int32 [S], or NULL: slot s reads row s of A (then
+ *             a_rows >= S). An index outside [0, a_rows) is the caller's
+ *             mistake: it is clamped into the range, never followed.
+ *   offsets   device int32 [E + 1], nondecreasing in [0, S] (clamped too).
+ *   Bq        device, E packed weights (e at Bq + e * w_bytes, see
+ *   scales    qgemm_mx_pack_device), their packed scales.
+ *   C         device, float or fp16 [S][N] per the epilogue.
+ *   epilogue  NULL, or as qgemm_run_ex with bias float [E][N] and residual
+ *             [S][N] in C's type (it may be C itself).
+ * workspace: as qgemm_run_ex, of qgemm_grouped_workspace_size() bytes. No
+ * host synchronisation: the sizes of the groups stay on the GPU.
+ * Errors: ERR_FORMAT (any other format), ERR_SHAPE, ERR_NULL, ERR_ALIGN,
+ * ERR_SIZE, ERR_DEVICE, ERR_NOMEM, ERR_LAUNCH. S, N or a_rows 0 is a no-op
+ * (no rows to read means no slot).
+ */
+qgemm_status qgemm_grouped_workspace_size(int S, int a_rows, int K, int N, int E, qgemm_format f,
+                                          size_t *bytes);
+qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_format f, const void *A,
+                               const int32_t *rows, const int32_t *offsets, const void *Bq,
+                               const void *scales, void *C, const qgemm_epilogue *epilogue,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ *   Y        device [S][N], float or fp16 (y_type QGEMM_TYPE_F32 / _F16).
+ *   slots    device int32 [T][topk]; a slot outside [0, S) adds nothing.
+ *   weights  device float [T][topk].
+ *   C        device [T][N], float or fp16 (c_type), fully written:
+ *            C[t] = sum over j ascending of weights[t][j] * Y[slots[t][j]], in
+ *            fp32 fused multiply-adds, rounded once; zeros for a token
+ *            without slots. The weight of a choice without slot is not used.
+ * C may not overlap Y. Errors: ERR_FORMAT (another type), ERR_SHAPE, ERR_NULL,
+ * ERR_ALIGN, ERR_DEVICE, ERR_LAUNCH. T or N 0 is a no-op.
+ */
+qgemm_status qgemm_group_combine(int T, int topk, int N, int S, const void *Y, int y_type,
+                                 const int32_t *slots, const float *weights, void *C, int c_type,
+                                 void *stream);
 
 #ifdef __cplusplus
 }

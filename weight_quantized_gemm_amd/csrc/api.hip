@@ -65,6 +65,7 @@ static qgemm_status check_run(int M, int K, int N, qgemm_format f, const void *A
     if (M < 0 || M > (1 << 24)) return QGEMM_ERR_SHAPE;
     *empty = (M == 0 || N == 0);
     if (*empty) return QGEMM_OK;
+    if (is_mx(f) && mx_grid(M, 1, N) > 0x7FFFFFFFLL) return QGEMM_ERR_SHAPE;
     if (!C) return QGEMM_ERR_NULL;
     if (K > 0 && (!A || !Bq)) return QGEMM_ERR_NULL;
     if (f == QGEMM_F32 || f == QGEMM_F16) {   // float weights: no pairs
@@ -118,7 +119,7 @@ static bool use_gemv(qgemm_format f, int M, int K, int N) {
                (M <= 4 || (long long)M * K * N <= (K <= 4096 ? kGemvInt4HalfMaxMKN : kGemvInt4MaxMKN));
     if (f == QGEMM_W4A8) return K <= kGemvMaxK;
     if (f == QGEMM_F16) return K <= kGemvF16MaxK;
-    return false;
+    return is_mx(f);
 }
 
 // What one call does, decided once from the shape and the GEMV limit in force
@@ -130,11 +131,11 @@ struct CallPlan {
     bool gemv;
     RunWorkspace r;
     int nsplit() const { return gemv ? r.gemv_nsplit : r.nsplit; }
-    // Scratch bytes the call touches: the W4A8 activation codes first, then
+    // Scratch bytes the call touches: the W4A8 or MXFP4_A4 activation codes first, then
     // (when the kernel splits K) the partial tiles. The size reported to
     // callers (run_workspace().bytes) is a function of the shape alone and
     // never smaller than this.
-    size_t used_bytes() const { return nsplit() <= 1 ? r.w4a8.bytes : r.bytes; }
+    size_t used_bytes() const { return nsplit() <= 1 ? r.act_bytes : r.bytes; }
 };
 
 static CallPlan plan_call(qgemm_format f, int M, int K, int N) {
@@ -189,6 +190,13 @@ static qgemm_status dispatch(int M, int K, int N, qgemm_format f, const Geometry
     case QGEMM_F16:
         return launched(gemv ? launch_gemv_f16(M, K, N, A, Bq, C, epi, s)
                              : launch_gemm_f16(M, K, N, A, Bq, C, epi, nsplit, part, s));
+    case QGEMM_MXFP4:      // one group of M rows
+    case QGEMM_MXFP4_A4:
+        return launched(launch_mx_gemm(f, MxArgs{M, M, K, N, 1, A, nullptr, nullptr,
+                                                 static_cast<const uint8_t *>(Bq),
+                                                 static_cast<const uint8_t *>(scales), 0, 0, C, epi, nullptr,
+                                                 nullptr, 0},
+                                       ws, s));
     default:
         break;
     }
@@ -224,6 +232,31 @@ static qgemm_status scratch_address(void **out) {
     }
     *out = p;
     return QGEMM_OK;
+}
+
+// Runs `work(scratch)` with the caller's workspace or, with NULL and 0, with
+// `need` bytes allocated and released in stream order.
+template <class F>
+static qgemm_status with_scratch(size_t need, void *workspace, size_t ws_bytes, hipStream_t s, F work) {
+    if (need == 0 || workspace || ws_bytes) return work(workspace);
+    void *ws = nullptr;
+    if (hipMallocAsync(&ws, need, s) != hipSuccess || !ws) {
+        (void)hipGetLastError();
+        return QGEMM_ERR_NOMEM;
+    }
+    qgemm_status st = work(ws);
+    if (hipFreeAsync(ws, s) != hipSuccess) {
+        (void)hipGetLastError();
+        if (st == QGEMM_OK) st = QGEMM_ERR_LAUNCH;
+    }
+    return st;
+}
+
+static qgemm_status check_scratch(size_t need, const void *workspace, size_t ws_bytes) {
+    if (need == 0 || (!workspace && ws_bytes == 0)) return QGEMM_OK;
+    if (!workspace) return QGEMM_ERR_NULL;
+    if (!aligned16(workspace)) return QGEMM_ERR_ALIGN;
+    return ws_bytes < need ? QGEMM_ERR_SIZE : QGEMM_OK;
 }
 
 }  // namespace qg
@@ -352,9 +385,10 @@ qgemm_status qgemm_w4a8_debug(int M, int K, int N, const void *A, const void *Bq
 }
 
 // Checks shared by the device quantisers; *empty is set for N == 0.
-static qgemm_status check_quantize(int K, int N, qgemm_format f, const float *W, const void *q,
+static qgemm_status check_quantize(int K, int N, qgemm_format f, bool packed, const float *W, const void *q,
                                    const void *pairs, Geometry *g, bool *empty) {
     if (f == QGEMM_F32 || f == QGEMM_F16) return QGEMM_ERR_FORMAT;   // float weights are not quantised
+    if (is_mx(f) && !packed) return QGEMM_ERR_FORMAT;                // scale bytes, not pairs
     qgemm_status st = geometry(K, N, f, g);
     if (st != QGEMM_OK) return st;
     // blocked formats: blocks of 16, 32 or a multiple of 64 (other multiples
@@ -373,7 +407,7 @@ qgemm_status qgemm_quantize_weights_device(int K, int N, qgemm_format f, const f
                                            void *q, float *pairs, void *stream) {
     Geometry g;
     bool empty = false;
-    qgemm_status st = check_quantize(K, N, f, W, q, pairs, &g, &empty);
+    qgemm_status st = check_quantize(K, N, f, false, W, q, pairs, &g, &empty);
     if (st != QGEMM_OK || empty) return st;
     (void)hipGetLastError();
     return launched(launch_quantize(K, N, f, false, W, q, pairs, g, static_cast<hipStream_t>(stream)));
@@ -383,11 +417,163 @@ qgemm_status qgemm_quantize_pack_device(int K, int N, qgemm_format f, const floa
                                         void *scales, void *stream) {
     Geometry g;
     bool empty = false;
-    qgemm_status st = check_quantize(K, N, f, W, Bq, scales, &g, &empty);
+    qgemm_status st = check_quantize(K, N, f, true, W, Bq, scales, &g, &empty);
     if (st != QGEMM_OK || empty) return st;
     (void)hipGetLastError();
+    if (is_mx(f)) return launched(launch_mx_quantize_pack(K, N, W, Bq, scales, static_cast<hipStream_t>(stream)));
     return launched(launch_quantize(K, N, f, true, W, Bq, static_cast<float *>(scales), g,
                                     static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// MXFP4 conversions
+// ---------------------------------------------------------------------------
+// Checks shared by the device conversions of R rows of K elements with row
+// stride ld; *empty is set where there is nothing to do.
+static qgemm_status check_mx_rows(int R, int K, int t, const void *X, long long ld, const void *q,
+                                  const void *scales, bool *empty) {
+    if (t != QGEMM_TYPE_F32 && t != QGEMM_TYPE_F16 && t != QGEMM_TYPE_BF16) return QGEMM_ERR_FORMAT;
+    if (R < 0 || K < 0 || R > (1 << 24) || K > (1 << 24) || K % 32 != 0) return QGEMM_ERR_SHAPE;
+    *empty = R == 0 || K == 0;
+    if (*empty) return QGEMM_OK;
+    if (ld < K || ld > (1LL << 38)) return QGEMM_ERR_SHAPE;
+    if (!X || !q || !scales) return QGEMM_ERR_NULL;
+    if (!aligned16(X) || !aligned16(q) || !aligned16(scales)) return QGEMM_ERR_ALIGN;
+    if (R > 1 && ld * (t == QGEMM_TYPE_F32 ? 4 : 2) % 16 != 0) return QGEMM_ERR_ALIGN;
+    return check_device();
+}
+
+qgemm_status qgemm_mx_quantize_device(int R, int K, int t, const void *X, long long ldx, uint8_t *q,
+                                      uint8_t *scales, void *stream) {
+    bool empty = false;
+    const qgemm_status st = check_mx_rows(R, K, t, X, ldx, q, scales, &empty);
+    if (st != QGEMM_OK || empty) return st;
+    (void)hipGetLastError();
+    return launched(launch_mx_quantize(R, K, t, X, (size_t)ldx, q, scales, static_cast<hipStream_t>(stream)));
+}
+
+qgemm_status qgemm_mx_dequantize_device(int R, int K, const uint8_t *q, const uint8_t *scales, int t, void *Y,
+                                        long long ldy, void *stream) {
+    bool empty = false;
+    const qgemm_status st = check_mx_rows(R, K, t, Y, ldy, q, scales, &empty);
+    if (st != QGEMM_OK || empty) return st;
+    (void)hipGetLastError();
+    return launched(launch_mx_dequantize(R, K, q, scales, t, Y, (size_t)ldy, static_cast<hipStream_t>(stream)));
+}
+
+qgemm_status qgemm_mx_pack_device(int K, int N, int E, const uint8_t *q, const uint8_t *scales, void *w_packed,
+                                  void *s_packed, void *stream) {
+    Geometry g;
+    qgemm_status st = geometry(K, N, QGEMM_MXFP4, &g);
+    if (st != QGEMM_OK) return st;
+    if (E < 0 || E > QGEMM_MAX_EXPERTS) return QGEMM_ERR_SHAPE;
+    if (N == 0 || E == 0) return QGEMM_OK;
+    if (!q || !scales || !w_packed || !s_packed) return QGEMM_ERR_NULL;
+    if (!aligned16(q) || !aligned16(scales) || !aligned16(w_packed) || !aligned16(s_packed)) return QGEMM_ERR_ALIGN;
+    st = check_device();
+    if (st != QGEMM_OK) return st;
+    (void)hipGetLastError();
+    return launched(launch_mx_pack(K, N, E, q, scales, w_packed, s_packed, g.w_bytes, g.s_bytes,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Mixture of experts
+// ---------------------------------------------------------------------------
+qgemm_status qgemm_group_plan_size(int T, int topk, int E, size_t *bytes) {
+    if (T < 0 || topk < 0 || E < 1 || E > QGEMM_MAX_EXPERTS || (long long)T * topk > (1LL << 26))
+        return QGEMM_ERR_SHAPE;
+    if (!bytes) return QGEMM_ERR_NULL;
+    const int G = plan_groups((long long)T * topk);
+    *bytes = G > 1 ? round_up((size_t)G * (E + 1) * sizeof(int32_t), kPackAlign) : 0;
+    return QGEMM_OK;
+}
+
+qgemm_status qgemm_group_plan(int T, int topk, int E, const void *ids, int ids64, int32_t *offsets, int32_t *rows,
+                              int32_t *slots, void *workspace, size_t ws_bytes, void *stream) {
+    size_t need = 0;
+    qgemm_status st = qgemm_group_plan_size(T, topk, E, &need);
+    if (st != QGEMM_OK) return st;
+    const int S = T * topk;
+    if (!offsets || (S > 0 && (!ids || !rows || !slots))) return QGEMM_ERR_NULL;
+    if (!aligned16(offsets) || (S > 0 && (!aligned16(ids) || !aligned16(rows) || !aligned16(slots))))
+        return QGEMM_ERR_ALIGN;
+    st = check_scratch(need, workspace, ws_bytes);
+    if (st != QGEMM_OK) return st;
+    st = check_device();
+    if (st != QGEMM_OK) return st;
+    (void)hipGetLastError();
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_scratch(need, workspace, ws_bytes, s, [&](void *ws) {
+        return launched(launch_group_plan(S, topk > 0 ? topk : 1, E, ids, ids64 != 0, offsets, rows, slots,
+                                          static_cast<int32_t *>(ws), s));
+    });
+}
+
+static qgemm_status check_grouped(int S, int a_rows, int K, int N, int E, qgemm_format f, Geometry *g) {
+    if (!is_mx(f)) return QGEMM_ERR_FORMAT;
+    const qgemm_status st = geometry(K, N, f, g);
+    if (st != QGEMM_OK) return st;
+    if (S < 0 || S > (1 << 26) || a_rows < 0 || a_rows > (1 << 26) || E < 1 || E > QGEMM_MAX_EXPERTS)
+        return QGEMM_ERR_SHAPE;
+    return mx_grid(S, E, N) > 0x7FFFFFFFLL ? QGEMM_ERR_SHAPE : QGEMM_OK;
+}
+
+qgemm_status qgemm_grouped_workspace_size(int S, int a_rows, int K, int N, int E, qgemm_format f, size_t *bytes) {
+    Geometry g;
+    const qgemm_status st = check_grouped(S, a_rows, K, N, E, f, &g);
+    if (st != QGEMM_OK) return st;
+    if (!bytes) return QGEMM_ERR_NULL;
+    *bytes = S > 0 && N > 0 ? mx_workspace(f, a_rows, K).bytes : 0;
+    return QGEMM_OK;
+}
+
+qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_format f, const void *A,
+                               const int32_t *rows, const int32_t *offsets, const void *Bq, const void *scales,
+                               void *C, const qgemm_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                               void *stream) {
+    Geometry g;
+    qgemm_status st = check_grouped(S, a_rows, K, N, E, f, &g);
+    if (st != QGEMM_OK) return st;
+    if (S == 0 || N == 0 || a_rows == 0) return QGEMM_OK;
+    if (!rows && a_rows < S) return QGEMM_ERR_SHAPE;
+    if (!A || !offsets || !Bq || !scales || !C) return QGEMM_ERR_NULL;
+    if (!aligned16(A) || !aligned16(offsets) || (rows && !aligned16(rows)) || !aligned16(Bq) || !aligned16(scales) ||
+        !aligned16(C))
+        return QGEMM_ERR_ALIGN;
+    Epilogue epi;
+    st = make_epilogue(epilogue, &epi);
+    if (st != QGEMM_OK) return st;
+    const size_t need = mx_workspace(f, a_rows, K).bytes;
+    st = check_scratch(need, workspace, ws_bytes);
+    if (st != QGEMM_OK) return st;
+    st = check_device();
+    if (st != QGEMM_OK) return st;
+    (void)hipGetLastError();
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const MxArgs args{S, a_rows, K, N, E, A, rows, offsets,
+                      static_cast<const uint8_t *>(Bq), static_cast<const uint8_t *>(scales), g.w_bytes, g.s_bytes,
+                      C, epi, nullptr, nullptr, 0};
+    return with_scratch(need, workspace, ws_bytes, s,
+                        [&](void *ws) { return launched(launch_mx_gemm(f, args, ws, s)); });
+}
+
+qgemm_status qgemm_group_combine(int T, int topk, int N, int S, const void *Y, int y_type, const int32_t *slots,
+                                 const float *weights, void *C, int c_type, void *stream) {
+    if ((y_type != QGEMM_TYPE_F32 && y_type != QGEMM_TYPE_F16) || (c_type != QGEMM_TYPE_F32 && c_type != QGEMM_TYPE_F16))
+        return QGEMM_ERR_FORMAT;
+    if (T < 0 || topk < 0 || N < 0 || S < 0 || T > (1 << 26) || N > (1 << 24) || S > (1 << 26) ||
+        (long long)T * topk > (1LL << 26) || (long long)T * div_up(N, 256) > 0x7FFFFFFFLL)
+        return QGEMM_ERR_SHAPE;
+    if (T == 0 || N == 0) return QGEMM_OK;
+    if (!C || (topk > 0 && (!slots || !weights || (S > 0 && !Y)))) return QGEMM_ERR_NULL;
+    if (!aligned16(C) || (topk > 0 && (!aligned16(slots) || !aligned16(weights) || (S > 0 && !aligned16(Y)))))
+        return QGEMM_ERR_ALIGN;
+    const qgemm_status st = check_device();
+    if (st != QGEMM_OK) return st;
+    (void)hipGetLastError();
+    return launched(launch_group_combine(T, topk, N, S, Y, y_type == QGEMM_TYPE_F16, slots, weights, C,
+                                         c_type == QGEMM_TYPE_F16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -16,7 +16,7 @@ namespace qg {
 
 static bool valid_format(int f) {
     return f == QGEMM_F32 || f == QGEMM_INT4_B64 || f == QGEMM_INT8_B0 || f == QGEMM_W4A8 ||
-           f == QGEMM_F16 || f == QGEMM_INT4_B0 || is_int4_blocked(f) || is_int8_blocked(f);
+           f == QGEMM_F16 || f == QGEMM_INT4_B0 || is_mx(f) || is_int4_blocked(f) || is_int8_blocked(f);
 }
 
 // Shapes are capped so that every element count and byte offset the kernels
@@ -25,8 +25,9 @@ constexpr int kMaxDim = 1 << 24;
 // W4A8 keeps D = sum_k qa * q in int32: |D| <= K * 127 * 15 must stay < 2^31.
 constexpr long long kW4A8MaxK = ((1LL << 31) - 1) / (127 * 15);
 
-// The quantised formats carry [offset, scale] pairs; float weights do not.
-static bool has_pairs(qgemm_format f) { return f != QGEMM_F32 && f != QGEMM_F16; }
+// The quantised formats carry [offset, scale] pairs; float weights do not, and
+// the MXFP4 formats carry scale bytes.
+static bool has_pairs(qgemm_format f) { return f != QGEMM_F32 && f != QGEMM_F16 && !is_mx(f); }
 
 qgemm_status geometry(int K, int N, qgemm_format f, Geometry *g) {
     if (!valid_format(f)) return QGEMM_ERR_FORMAT;
@@ -86,6 +87,13 @@ qgemm_status geometry(int K, int N, qgemm_format f, Geometry *g) {
         r.w_bytes = round_up((size_t)(r.Np / 32) * (K / 64) * 1024, kPackAlign);
         r.s_bytes = round_up((size_t)(r.Np / 32) * (K / 64) * 256, kPackAlign);
         break;
+    case QGEMM_MXFP4:
+    case QGEMM_MXFP4_A4:
+        if (K == 0 || K % 64 != 0) return QGEMM_ERR_SHAPE;
+        r.Kp = K; r.Np = (int)round_up(N, 32); r.nblk = K / 32; r.block = 32;
+        r.w_bytes = round_up((size_t)(r.Np / 32) * (K / 64) * 1024, kPackAlign);
+        r.s_bytes = (size_t)(r.Np / 32) * (round_up(K, 256) / 256) * 256;
+        break;
     case QGEMM_INT8_B0:
         if (K == 0) return QGEMM_ERR_SHAPE;
         r.Kp = (int)round_up(K, 64); r.Np = (int)round_up(N, 4); r.nblk = 1; r.block = K;
@@ -111,6 +119,20 @@ W4A8Workspace w4a8_workspace(int M, int K) {
     w.S_off = w.sa_off + round_up((size_t)M * sizeof(float), kPackAlign);
     w.bytes = w.S_off + round_up((size_t)M * sizeof(int32_t), kPackAlign);
     return w;
+}
+
+MxWorkspace mx_workspace(qgemm_format f, long long rows, int K) {
+    MxWorkspace w{0, 0, 0};
+    if (f != QGEMM_MXFP4_A4) return w;
+    const size_t n256 = round_up(K, 256) / 256;
+    w.s_off = round_up((size_t)rows * n256 * 128, kPackAlign);
+    w.bytes = w.s_off + round_up((size_t)rows * n256 * 8, kPackAlign);
+    return w;
+}
+
+long long mx_grid(int S, int E, int N) {
+    const long long groups = E < S ? E : S;
+    return (groups + (S - groups) / 32) * div_up(N, 128);
 }
 
 int f32_kgroups(int M, int N) {
@@ -226,7 +248,8 @@ RunWorkspace run_workspace(qgemm_format f, int M, int K, int N) {
     r.nsplit = splitk_plan(f, M, K, N);
     r.gemv_nsplit = gemv_split_plan(f, M, K, N);
     const int most = r.nsplit > r.gemv_nsplit ? r.nsplit : r.gemv_nsplit;
-    r.part_off = round_up(r.w4a8.bytes, kPackAlign);
+    r.act_bytes = is_mx(f) ? mx_workspace(f, M, K).bytes : r.w4a8.bytes;
+    r.part_off = round_up(r.act_bytes, kPackAlign);
     r.part_bytes = most > 1 ? round_up((size_t)most * M * N * 4, kPackAlign) : 0;
     r.bytes = r.part_off + r.part_bytes;
     return r;
@@ -281,6 +304,7 @@ qgemm_status qgemm_canonical_size(int K, int N, qgemm_format f, size_t *q_bytes,
     Geometry g;
     qgemm_status st = geometry(K, N, f, &g);
     if (st != QGEMM_OK) return st;
+    if (is_mx(f)) return QGEMM_ERR_FORMAT;        // scale bytes, not pairs
     if (!q_bytes || !pair_floats) return QGEMM_ERR_NULL;
     *q_bytes = canonical_q_bytes(g, f);
     *pair_floats = canonical_pair_floats(g, f);
@@ -369,6 +393,7 @@ qgemm_status qgemm_pack_weights(int K, int N, qgemm_format f, const void *w_cano
     Geometry g;
     qgemm_status st = geometry(K, N, f, &g);
     if (st != QGEMM_OK) return st;
+    if (is_mx(f)) return QGEMM_ERR_FORMAT;        // scale bytes: qgemm_mx_pack
     if (!w_packed || (g.s_bytes && !s_packed)) return QGEMM_ERR_NULL;
     if (w_bytes < g.w_bytes || s_bytes < g.s_bytes) return QGEMM_ERR_SIZE;
     if ((size_t)N * K > 0 && !w_canonical) return QGEMM_ERR_NULL;
@@ -478,6 +503,7 @@ qgemm_status qgemm_unpack_weights(int K, int N, qgemm_format f, const void *w_pa
     Geometry g;
     qgemm_status st = geometry(K, N, f, &g);
     if (st != QGEMM_OK) return st;
+    if (is_mx(f)) return QGEMM_ERR_FORMAT;        // scale bytes, not pairs
     if (!w_packed || (g.s_bytes && !s_packed)) return QGEMM_ERR_NULL;
     if (w_bytes < g.w_bytes || s_bytes < g.s_bytes) return QGEMM_ERR_SIZE;
     if ((size_t)N * K > 0 && !w_canonical) return QGEMM_ERR_NULL;
@@ -569,6 +595,65 @@ qgemm_status qgemm_unpack_weights(int K, int N, qgemm_format f, const void *w_pa
         break;
     }
     }
+    return QGEMM_OK;
+}
+
+// ---------------------------------------------------------------------------
+// MXFP4 (see qgemm.h for the rules)
+// ---------------------------------------------------------------------------
+qgemm_status qgemm_mx_quantize(int R, int K, const float *X, uint8_t *q, uint8_t *scales) {
+    if (R < 0 || K < 0 || R > kMaxDim || K > kMaxDim || K % 32 != 0) return QGEMM_ERR_SHAPE;
+    if (R == 0 || K == 0) return QGEMM_OK;
+    if (!X || !q || !scales) return QGEMM_ERR_NULL;
+    const size_t total = (size_t)R * K;
+    for (size_t i = 0; i < total; ++i)
+        if (!std::isfinite(X[i])) return QGEMM_ERR_VALUE;
+    for (size_t b = 0; b < total / 32; ++b) {
+        const float *x = X + 32 * b;
+        float top = 0.0f;
+        for (int i = 0; i < 32; ++i) top = std::fmax(top, std::fabs(x[i]));
+        int e = -127;
+        if (top > 0.0f) {
+            int ex = 0;
+            (void)std::frexp(top, &ex);             // top in [2^(ex - 1), 2^ex)
+            e = ex - 1 - 2;
+            if (e < -127) e = -127;
+        }
+        scales[b] = (uint8_t)(e + 127);
+        for (int i = 0; i < 32; i += 2) {
+            unsigned byte = 0;
+            for (int k = 0; k < 2; ++k) {
+                // exact: a double holds every fp32 times any power of two here
+                const double y = std::ldexp(std::fabs((double)x[i + k]), -e);
+                unsigned c = (y > 0.25) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0);
+                if (std::signbit(x[i + k])) c |= 8u;
+                byte |= c << (4 * k);
+            }
+            q[16 * b + i / 2] = (uint8_t)byte;
+        }
+    }
+    return QGEMM_OK;
+}
+
+qgemm_status qgemm_mx_pack(int K, int N, const uint8_t *q, const uint8_t *scales, void *w_packed, size_t w_bytes,
+                           void *s_packed, size_t s_bytes) {
+    Geometry g;
+    const qgemm_status st = geometry(K, N, QGEMM_MXFP4, &g);
+    if (st != QGEMM_OK) return st;
+    if (N == 0) return QGEMM_OK;
+    if (!q || !scales || !w_packed || !s_packed) return QGEMM_ERR_NULL;
+    if (w_bytes < g.w_bytes || s_bytes < g.s_bytes) return QGEMM_ERR_SIZE;
+    uint8_t *wp = static_cast<uint8_t *>(w_packed), *sp = static_cast<uint8_t *>(s_packed);
+    std::memset(wp, 0, g.w_bytes);
+    std::memset(sp, 0, g.s_bytes);
+    const unsigned n64 = (unsigned)K / 64, n256 = ((unsigned)K + 255) / 256;
+    for (int n = 0; n < N; ++n)
+        for (unsigned b = 0; b < n64; ++b)
+            for (unsigned h = 0; h < 2; ++h) {
+                std::memcpy(wp + ((size_t)(n >> 5) * n64 + b) * 1024 + (32 * h + (n & 31)) * 16,
+                            q + (size_t)n * (K / 2) + 32 * b + 16 * h, 16);
+                sp[mx_weight_scale(n, b, h, n256)] = scales[(size_t)n * (K / 32) + 2 * b + h];
+            }
     return QGEMM_OK;
 }
 

@@ -53,6 +53,15 @@ constexpr size_t kPackAlign = 256;
 //            of a 32 x 32 x 32 int8 MFMA operand (lane = 32 h + c).
 //   pairs:   [Np][2] floats.
 // F32: weights = B float [K][N] unchanged; no pairs.
+// MXFP4 (both formats), n64 = K / 64, n256 = ceil(K / 256), Np = roundup(N, 32):
+//   weights: 1 KiB records as INT4_B64's; piece 32 h + c is the 32 codes of
+//            one scaled block, and a record is one operand of the 32 x 32 x 64
+//            scaled MFMA;
+//   scales:  256-byte records, record (t, g) at (t * n256 + g) * 256 for the
+//            channels 32 t .. + 31 and k in [256 g, 256 g + 256): byte
+//            4 (32 h + c) + j is the scale of channel 32 t + c, k = 256 g +
+//            64 j + 32 h .. + 31 (zero past K), so a lane's word holds four
+//            consecutive records' scales.
 // ---------------------------------------------------------------------------
 struct Geometry {
     int K = 0, N = 0;
@@ -87,6 +96,7 @@ inline bool is_int4_blocked(int f) {
     return f > QGEMM_INT4_BLOCK_BASE && f <= QGEMM_INT4_BLOCK_BASE + kMaxBlock;
 }
 // Int8 with a block size in the format id (QGEMM_INT8_BLOCK(b)).
+inline bool is_mx(int f) { return f == QGEMM_MXFP4 || f == QGEMM_MXFP4_A4; }
 inline bool is_int8_blocked(int f) {
     return f > QGEMM_INT8_BLOCK_BASE && f <= QGEMM_INT8_BLOCK_BASE + kMaxBlock;
 }
@@ -262,12 +272,74 @@ int splitk_plan(qgemm_format f, int M, int K, int N);      // 1 = no split
 // 32-channel tiles split K over the workgroups of a tile.
 int gemv_split_plan(qgemm_format f, int M, int K, int N);
 
-// Full scratch layout of one call: the W4A8 part (if any) first, then the
+// ---------------------------------------------------------------------------
+// MXFP4 and the operators of mixture-of-experts layers.
+// ---------------------------------------------------------------------------
+// Byte of block (32-element half h of 64-element block b) of row r in the
+// activation scales: [row][K / 256][h][4], so that lane (row, h) of a matrix
+// operand finds the scales of four consecutive 64-blocks in one word.
+__host__ __device__ inline size_t mx_act_scale(size_t r, unsigned b, unsigned h, unsigned n256) {
+    return ((r * n256 + (b >> 2)) * 2 + h) * 4 + (b & 3);
+}
+
+// The same for channel n of a packed weight: 256-byte records (32-channel
+// tile, 256 K-elements), word 32 h + channel, byte = 64-block of the four.
+__host__ __device__ inline size_t mx_weight_scale(size_t n, unsigned b, unsigned h, unsigned n256) {
+    return ((n >> 5) * n256 + (b >> 2)) * 256 + (32 * h + (n & 31)) * 4 + (b & 3);
+}
+
+// One product, dense or grouped: slots [0, S) of C, each reading row rows[s]
+// of A (s itself without `rows`), in E groups (see find_row_tile).
+struct MxArgs {
+    int S, a_rows, K, N, E;
+    const void *A;                    // fp16 [a_rows][K]
+    const int32_t *rows, *offsets;
+    const uint8_t *W, *Ws;            // packed weights and scales of group 0
+    size_t w_bytes, s_bytes;          // from one group's to the next
+    void *C;
+    Epilogue epi;
+    // set by the launcher
+    const uint8_t *Aq, *As;           // MXFP4_A4: activation codes [a_rows][Kp / 2] and
+                                      // scales [a_rows][Kp / 256][2][4], Kp = roundup(K, 256)
+    int tiles_n;
+};
+// MXFP4_A4 scratch: the codes of `rows` rows, then their scales.
+struct MxWorkspace {
+    size_t q_off, s_off, bytes;
+};
+MxWorkspace mx_workspace(qgemm_format f, long long rows, int K);
+// Workgroups of the product's launch (at most 2^31 - 1 are allowed).
+long long mx_grid(int S, int E, int N);
+hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, void *ws, hipStream_t s);
+
+hipError_t launch_mx_quantize(int R, int K, int t, const void *X, size_t ldx, uint8_t *q, uint8_t *scales,
+                              hipStream_t s);
+hipError_t launch_mx_quantize_act(int R, int K, const void *A, uint8_t *q, uint8_t *scales, hipStream_t s);
+hipError_t launch_mx_quantize_pack(int K, int N, const float *W, void *Bq, void *scales, hipStream_t s);
+hipError_t launch_mx_dequantize(int R, int K, const uint8_t *q, const uint8_t *scales, int t, void *Y,
+                                size_t ldy, hipStream_t s);
+hipError_t launch_mx_pack(int K, int N, int E, const uint8_t *q, const uint8_t *scales, void *wp, void *sp,
+                          size_t w_bytes, size_t s_bytes, hipStream_t s);
+
+// Workgroups of the plan for S choices: one while a single workgroup's waves
+// take at most 8 turns of 64 each, else one for every such load, up to 64.
+constexpr int kPlanOneMax = 8192;
+inline int plan_groups(long long S) {
+    const long long g = (S + kPlanOneMax - 1) / kPlanOneMax;
+    return g < 1 ? 1 : g > 64 ? 64 : (int)g;
+}
+hipError_t launch_group_plan(int S, int topk, int E, const void *ids, bool ids64, int32_t *offsets, int32_t *rows,
+                             int32_t *slots, int32_t *totals, hipStream_t s);
+hipError_t launch_group_combine(int T, int topk, int N, int S, const void *Y, bool y16, const int32_t *slots,
+                                const float *weights, void *C, bool c16, hipStream_t s);
+
+// Full scratch layout of one call: the W4A8 or MXFP4_A4 part (if any) first, then the
 // split-K partials [S][M][N] (4 bytes each), sized for the larger of the
 // tiled GEMM's plan (nsplit) and the GEMV's (gemv_nsplit), so that the size
 // is a function of the shape alone whichever kernel a call takes.
 struct RunWorkspace {
     W4A8Workspace w4a8;       // bytes == 0 unless W4A8
+    size_t act_bytes;         // the quantised activations: W4A8's or MXFP4_A4's, else 0
     int nsplit, gemv_nsplit;
     size_t part_off, part_bytes, bytes;
 };

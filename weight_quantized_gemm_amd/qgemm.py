@@ -22,10 +22,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqgemm.so")
 
 # Format ids (0-3: the MNN GemmSpeed page's mode numbers; 4: fp16 weights;
-# 5: Int4-Block0 with fp16 activations) and names.
+# 5: Int4-Block0 with fp16 activations; 6, 8: MXFP4 weights with fp16 / MXFP4
+# activations) and names.
 QGEMM_F32, QGEMM_INT4_B64, QGEMM_INT8_B0, QGEMM_W4A8, QGEMM_F16, QGEMM_INT4_B0 = 0, 1, 2, 3, 4, 5
+QGEMM_MXFP4, QGEMM_MXFP4_A4 = 6, 8
 FORMATS = {"f32": QGEMM_F32, "int4b64": QGEMM_INT4_B64, "int8b0": QGEMM_INT8_B0,
-           "w4a8": QGEMM_W4A8, "f16": QGEMM_F16, "int4b0": QGEMM_INT4_B0}
+           "w4a8": QGEMM_W4A8, "f16": QGEMM_F16, "int4b0": QGEMM_INT4_B0,
+           "mxfp4": QGEMM_MXFP4, "mxfp4a4": QGEMM_MXFP4_A4}
 
 STATUS = {0: "QGEMM_OK", 1: "QGEMM_ERR_NULL", 2: "QGEMM_ERR_SHAPE", 3: "QGEMM_ERR_FORMAT",
           4: "QGEMM_ERR_ALIGN", 5: "QGEMM_ERR_NOMEM", 6: "QGEMM_ERR_DEVICE",
@@ -36,7 +39,10 @@ EXPORTS = ["qgemm_status_string", "qgemm_abi_version", "qgemm_canonical_size",
            "qgemm_quantize_weights", "qgemm_packed_size", "qgemm_pack_weights",
            "qgemm_unpack_weights", "qgemm_workspace_size", "qgemm_run", "qgemm_run_ws",
            "qgemm_run_ex", "qgemm_run_noalloc", "qgemm_w4a8_debug", "qgemm_set_gemv_max_m",
-           "qgemm_quantize_weights_device", "qgemm_quantize_pack_device"]
+           "qgemm_quantize_weights_device", "qgemm_quantize_pack_device",
+           "qgemm_mx_quantize", "qgemm_mx_quantize_device", "qgemm_mx_dequantize_device",
+           "qgemm_mx_pack", "qgemm_mx_pack_device", "qgemm_group_plan_size", "qgemm_group_plan",
+           "qgemm_grouped_workspace_size", "qgemm_run_grouped", "qgemm_group_combine"]
 
 
 class QGemmError(RuntimeError):
@@ -58,7 +64,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             f"{path} is missing: build it with `python -m weight_quantized_gemm_amd.build_lib` "
             "(there is no fallback path)")
     lib = ctypes.CDLL(path)
-    P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
     ZP = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "qgemm_status_string": ([I], ctypes.c_char_p),
@@ -77,6 +83,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "qgemm_set_gemv_max_m": ([I], I),
         "qgemm_quantize_weights_device": ([I, I, I, P, P, P, P], I),
         "qgemm_quantize_pack_device": ([I, I, I, P, P, P, P], I),
+        "qgemm_mx_quantize": ([I, I, P, P, P], I),
+        "qgemm_mx_quantize_device": ([I, I, I, P, L, P, P, P], I),
+        "qgemm_mx_dequantize_device": ([I, I, P, P, I, P, L, P], I),
+        "qgemm_mx_pack": ([I, I, P, P, P, Z, P, Z], I),
+        "qgemm_mx_pack_device": ([I, I, I, P, P, P, P, P], I),
+        "qgemm_group_plan_size": ([I, I, I, ZP], I),
+        "qgemm_group_plan": ([I, I, I, P, I, P, P, P, P, Z, P], I),
+        "qgemm_grouped_workspace_size": ([I, I, I, I, I, I, ZP], I),
+        "qgemm_run_grouped": ([I, I, I, I, I, I, P, P, P, P, P, P, ctypes.POINTER(Epilogue), P, Z, P], I),
+        "qgemm_group_combine": ([I, I, I, I, P, I, P, P, P, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -396,16 +412,259 @@ def qgemm_set_gemv_max_m(max_m: int) -> int:
 
 
 # ---------------------------------------------------------------------------
+# MXFP4 conversions and mixture of experts. These take torch tensors only: the
+# sizes come from their shapes, and the call runs on the tensors' own device
+# (on its current stream unless one is given).
+# ---------------------------------------------------------------------------
+TYPES = {"f32": 0, "f16": 1, "bf16": 2}                  # qgemm_type
+_TORCH_TYPES = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
+_TYPE_IDS = {d: t for t, d in _TORCH_TYPES.items()}
+
+
+def _same_device(**tensors):
+    """Checks that the tensors (None passes) are GPU tensors of one device and
+    returns it."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name}: expected a GPU tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _exact(t, name: str, dtypes, shape):
+    """Checks a tensor's dtype, shape and contiguity."""
+    _need(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _row_stride(t, name: str) -> int:
+    """Row stride of a [R][K] tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: expected [R][K] with contiguous, ascending rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def qgemm_mx_quantize(X: np.ndarray):
+    """Host float X [R][K] -> (MXFP4 codes uint8 [R][K/2], scales uint8 [R][K/32])."""
+    X = np.ascontiguousarray(X, dtype=np.float32)
+    R, K = X.shape
+    q = np.zeros((R, K // 2), np.uint8)
+    scales = np.zeros((R, K // 32), np.uint8)
+    _check(load().qgemm_mx_quantize(R, K, _np_ptr(X), _np_ptr(q), _np_ptr(scales)), "qgemm_mx_quantize")
+    return q, scales
+
+
+def qgemm_mx_quantize_device(X, q=None, scales=None, stream=None):
+    """Device X [R][K] (fp32, fp16 or bf16, rows may be strided) -> (MXFP4 codes
+    uint8 [R][K/2], scales uint8 [R][K/32]), allocated here unless given."""
+    dev = _same_device(X=X, q=q, scales=scales)
+    if X.dtype not in _TYPE_IDS:
+        raise ValueError(f"X: dtype {X.dtype} where float32, float16 or bfloat16 is required")
+    ld = _row_stride(X, "X")
+    R, K = X.shape
+    if q is None:
+        q = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((R, K // 32), dtype=torch.uint8, device=dev)
+    _exact(q, "q", (torch.uint8,), (R, K // 2))
+    _exact(scales, "scales", (torch.uint8,), (R, K // 32))
+    with torch.cuda.device(dev):
+        _check(load().qgemm_mx_quantize_device(R, K, _TYPE_IDS[X.dtype], X.data_ptr(), ld, q.data_ptr(),
+                                               scales.data_ptr(), _stream(stream)), "qgemm_mx_quantize_device")
+    return q, scales
+
+
+def qgemm_mx_dequantize_device(q, scales, dtype="f32", Y=None, stream=None):
+    """Device MXFP4 codes [R][K/2] and scales [R][K/32] -> their values [R][K]
+    in dtype ("f32", "f16", "bf16"), or into Y (whose rows may be strided)."""
+    dev = _same_device(q=q, scales=scales, Y=Y)
+    if q.dim() != 2:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [R][K/2]")
+    R, K = q.shape[0], 2 * q.shape[1]
+    _exact(q, "q", (torch.uint8,), (R, K // 2))
+    _exact(scales, "scales", (torch.uint8,), (R, K // 32))
+    if Y is None:
+        if dtype not in TYPES:
+            raise ValueError(f"unknown type {dtype}")
+        Y = torch.empty((R, K), dtype=_TORCH_TYPES[TYPES[dtype]], device=dev)
+    if Y.dtype not in _TYPE_IDS or tuple(Y.shape) != (R, K):
+        raise ValueError(f"Y: {Y.dtype} {tuple(Y.shape)}, expected a float tensor of shape {(R, K)}")
+    ld = _row_stride(Y, "Y")
+    with torch.cuda.device(dev):
+        _check(load().qgemm_mx_dequantize_device(R, K, q.data_ptr(), scales.data_ptr(), _TYPE_IDS[Y.dtype],
+                                                 Y.data_ptr(), ld, _stream(stream)),
+               "qgemm_mx_dequantize_device")
+    return Y
+
+
+def qgemm_mx_pack(K: int, N: int, q: np.ndarray, scales: np.ndarray):
+    """Host canonical MXFP4 codes [N][K/2] and scales [N][K/32] -> (packed
+    weights uint8, packed scales uint8), host."""
+    wb, sb = qgemm_packed_size(K, N, QGEMM_MXFP4)
+    q = np.ascontiguousarray(q, dtype=np.uint8)
+    scales = np.ascontiguousarray(scales, dtype=np.uint8)
+    if q.size != N * (K // 2) or scales.size != N * (K // 32):
+        raise ValueError(f"q, scales: {q.size} and {scales.size} bytes, expected {N * (K // 2)} and {N * (K // 32)}")
+    wp, sp = np.empty(wb, np.uint8), np.empty(sb, np.uint8)
+    _check(load().qgemm_mx_pack(K, N, _np_ptr(q), _np_ptr(scales), _np_ptr(wp), wb, _np_ptr(sp), sb),
+           "qgemm_mx_pack")
+    return wp, sp
+
+
+def qgemm_mx_pack_device(K: int, N: int, q, scales, E: int = 1, Bq=None, Sp=None, stream=None):
+    """Device canonical MXFP4 codes [E][N][K/2] and scales [E][N][K/32] (or
+    without the first axis) -> (packed weights, packed scales) of all E
+    weights, uint8 device tensors, one weight after the other."""
+    dev = _same_device(q=q, scales=scales, Bq=Bq, Sp=Sp)
+    wb, sb = qgemm_packed_size(K, N, QGEMM_MXFP4)
+    _exact(q.reshape(-1), "q", (torch.uint8,), (E * N * (K // 2),))
+    _exact(scales.reshape(-1), "scales", (torch.uint8,), (E * N * (K // 32),))
+    q, scales = q.contiguous(), scales.contiguous()
+    if Bq is None:
+        Bq = torch.empty(E * wb, dtype=torch.uint8, device=dev)
+    if Sp is None:
+        Sp = torch.empty(E * sb, dtype=torch.uint8, device=dev)
+    _exact(Bq, "Bq", (torch.uint8,), (E * wb,))
+    _exact(Sp, "Sp", (torch.uint8,), (E * sb,))
+    with torch.cuda.device(dev):
+        _check(load().qgemm_mx_pack_device(K, N, E, q.data_ptr(), scales.data_ptr(), Bq.data_ptr(), Sp.data_ptr(),
+                                           _stream(stream)), "qgemm_mx_pack_device")
+    return Bq, Sp
+
+
+def qgemm_group_plan_size(T: int, topk: int, E: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().qgemm_group_plan_size(T, topk, E, ctypes.byref(b)), "qgemm_group_plan_size")
+    return b.value
+
+
+def _scratch(workspace, ws_bytes: int):
+    """Address of an optional workspace tensor that claims ws_bytes."""
+    if workspace is None:
+        return None
+    have = workspace.numel() * workspace.element_size()
+    if have < ws_bytes:
+        raise ValueError(f"workspace: {have} bytes, ws_bytes={ws_bytes} claimed")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace.data_ptr()
+
+
+def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace=None, ws_bytes: int = 0,
+                     stream=None):
+    """Expert ids [T][topk] (int32 or int64; an id outside [0, E) has no slot)
+    -> (offsets [E + 1], rows [T * topk], slots [T][topk]), int32, allocated
+    here unless given."""
+    dev = _same_device(ids=ids, offsets=offsets, rows=rows, slots=slots, workspace=workspace)
+    if ids.dim() != 2:
+        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T][topk]")
+    T, topk = ids.shape
+    _exact(ids, "ids", (torch.int32, torch.int64), (T, topk))
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+    if not 1 <= E <= 1024:
+        raise QGemmError(2, "qgemm_group_plan")
+    offsets = new(E + 1) if offsets is None else offsets
+    rows = new(T * topk) if rows is None else rows
+    slots = new(T, topk) if slots is None else slots
+    _exact(offsets, "offsets", (torch.int32,), (E + 1,))
+    _exact(rows, "rows", (torch.int32,), (T * topk,))
+    _exact(slots, "slots", (torch.int32,), (T, topk))
+    with torch.cuda.device(dev):
+        _check(load().qgemm_group_plan(T, topk, E, ids.data_ptr(), int(ids.dtype == torch.int64),
+                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+                                       _scratch(workspace, ws_bytes), ws_bytes, _stream(stream)),
+               "qgemm_group_plan")
+    return offsets, rows, slots
+
+
+def qgemm_grouped_workspace_size(S: int, a_rows: int, K: int, N: int, E: int, fmt) -> int:
+    b = ctypes.c_size_t()
+    _check(load().qgemm_grouped_workspace_size(S, a_rows, K, N, E, _fmt(fmt), ctypes.byref(b)),
+           "qgemm_grouped_workspace_size")
+    return b.value
+
+
+def qgemm_run_grouped(K: int, N: int, E: int, fmt, A, rows, offsets, Bq, scales, C, bias=None, residual=None,
+                      activation="none", out_type="f32", workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """C[s] = act(A[rows[s]] x deq(B_e) + bias[e] + residual[s]) for the slots s
+    of every expert e, offsets[e] <= s < offsets[e + 1]; A fp16 [a_rows][K],
+    rows int32 [S] or None (slot s reads row s), C [S][N] fp32 or fp16 per
+    out_type, bias fp32 [E][N], residual as C. Rows of C that no expert owns
+    are left as they were."""
+    dev = _same_device(A=A, rows=rows, offsets=offsets, Bq=Bq, scales=scales, C=C, bias=bias, residual=residual,
+                       workspace=workspace)
+    f = _fmt(fmt)
+    if C.dim() != 2 or A.dim() != 2:
+        raise ValueError("A, C: expected [a_rows][K] and [S][N]")
+    S, a_rows = C.shape[0], A.shape[0]
+    c_dt = torch.float16 if out_type in (1, "f16") else torch.float32
+    _exact(A, "A", (torch.float16,), (a_rows, K))
+    _exact(C, "C", (c_dt,), (S, N))
+    _exact(offsets, "offsets", (torch.int32,), (E + 1,))
+    if rows is not None:
+        _exact(rows, "rows", (torch.int32,), (S,))
+    if bias is not None:
+        _exact(bias, "bias", (torch.float32,), (E, N))
+    if residual is not None:
+        _exact(residual, "residual", (c_dt,), (S, N))
+    if f in (QGEMM_MXFP4, QGEMM_MXFP4_A4):     # the library refuses any other
+        wb, sb = qgemm_packed_size(K, N, f)
+        _exact(Bq, "Bq", (torch.uint8,), (E * wb,))
+        _exact(scales, "scales", (torch.uint8,), (E * sb,))
+    epi = Epilogue(_dev_ptr(bias), _dev_ptr(residual),
+                   ACTIVATIONS[activation] if isinstance(activation, str) else int(activation),
+                   OUT_TYPES[out_type] if isinstance(out_type, str) else int(out_type))
+    with torch.cuda.device(dev):
+        _check(load().qgemm_run_grouped(S, a_rows, K, N, E, f, A.data_ptr(), _dev_ptr(rows), offsets.data_ptr(),
+                                        Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi),
+                                        _scratch(workspace, ws_bytes), ws_bytes, _stream(stream)),
+               "qgemm_run_grouped")
+
+
+def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
+    """C[t] = sum over j of weights[t][j] * Y[slots[t][j]] (a slot outside Y adds
+    nothing); Y [S][N] and C [T][N] fp32 or fp16, slots int32 and weights fp32
+    [T][topk]."""
+    dev = _same_device(Y=Y, slots=slots, weights=weights, C=C)
+    if Y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("Y, slots: expected [S][N] and [T][topk]")
+    (S, N), (T, topk) = Y.shape, slots.shape
+    half = (torch.float32, torch.float16)
+    _exact(Y, "Y", half, (S, N))
+    _exact(slots, "slots", (torch.int32,), (T, topk))
+    _exact(weights, "weights", (torch.float32,), (T, topk))
+    _exact(C, "C", half, (T, N))
+    with torch.cuda.device(dev):
+        _check(load().qgemm_group_combine(T, topk, N, S, Y.data_ptr(), _TYPE_IDS[Y.dtype], slots.data_ptr(),
+                                          weights.data_ptr(), C.data_ptr(), _TYPE_IDS[C.dtype], _stream(stream)),
+               "qgemm_group_combine")
+
+
+# ---------------------------------------------------------------------------
 # Convenience: a packed weight resident on the GPU.
 # ---------------------------------------------------------------------------
 class PackedWeight:
-    """Quantise (or take) a weight, pack it and upload it to the GPU."""
+    """Quantise (or take) a weight, pack it and upload it to the GPU. For the
+    MXFP4 formats the pairs are the scale bytes [N][K/32]."""
 
     def __init__(self, fmt, K: int, N: int, w_canonical: np.ndarray,
                  pairs_canonical: np.ndarray | None, device="cuda"):
         self.fmt = _fmt(fmt)
         self.K, self.N = K, N
-        wp, sp = qgemm_pack_weights(K, N, self.fmt, w_canonical, pairs_canonical)
+        if self.fmt in (QGEMM_MXFP4, QGEMM_MXFP4_A4):
+            wp, sp = qgemm_mx_pack(K, N, w_canonical, pairs_canonical)
+        else:
+            wp, sp = qgemm_pack_weights(K, N, self.fmt, w_canonical, pairs_canonical)
         self.Bq = torch.from_numpy(wp).to(device)
         self.scales = torch.from_numpy(sp).to(device) if sp.size else None
 
@@ -416,7 +675,7 @@ class PackedWeight:
         N, K = W.shape
         if f == QGEMM_F32:
             return cls(f, K, N, np.ascontiguousarray(W.T, dtype=np.float32), None, device)
-        q, pairs = qgemm_quantize_weights(W, f)
+        q, pairs = qgemm_mx_quantize(W) if f in (QGEMM_MXFP4, QGEMM_MXFP4_A4) else qgemm_quantize_weights(W, f)
         return cls(f, K, N, q, pairs, device)
 
     def __call__(self, A: torch.Tensor, C: torch.Tensor | None = None, stream=None):
