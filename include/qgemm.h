@@ -119,7 +119,8 @@ typedef enum qgemm_status {
     QGEMM_OK = 0,
     QGEMM_ERR_NULL = 1,     /* a required pointer is NULL                     */
     QGEMM_ERR_SHAPE = 2,    /* a shape is negative, too large, or violates the
-                               format's block rule (INT4_B64, MXFP4: K % 64 == 0;
+                               format's block rule (INT4_B64, MXFP4: K % 64 == 0,
+                               MXFP4 also K <= 2^22;
                                INT4/W4A8: K even; quantised formats: K > 0)   */
     QGEMM_ERR_FORMAT = 3,   /* unknown format or type, or an operation the format does
                                not have (e.g. quantising to F32)              */
@@ -502,7 +503,8 @@ qgemm_status qgemm_group_plan(int T, int topk, int E, const void *ids, int ids64
  *   f         QGEMM_MXFP4 or QGEMM_MXFP4_A4.
  *   A         device fp16 [a_rows][K].
  *   rows      device int32 [S], or NULL: slot s reads row s of A (then
- *             a_rows >= S). An index outside [0, a_rows) is the caller's
+ *             a_rows >= S). With it, A (or for MXFP4_A4 its codes, a quarter
+ *             of that) may have at most 2^32 - 1 bytes. An index outside [0, a_rows) is the caller's
  *             mistake: it is clamped into the range, never followed.
  *   offsets   device int32 [E + 1], nondecreasing in [0, S] (clamped too).
  *   Bq        device, E packed weights (e at Bq + e * w_bytes, see

@@ -148,6 +148,17 @@ def test_activation_scratch_is_reported():
     assert Q.qgemm_grouped_workspace_size(400, 64, 320, 64, 4, "mxfp4a4") >= 64 * (512 // 2 + 512 // 32)
 
 
+@pytest.mark.parametrize("K", [64, 256, 320, 1024, 2560, 4096, 9728])
+def test_activation_scratch_covers_the_widest_read(K):
+    """The kernels fetch the scales of four 256-element groups at once, starting
+    at any group of a row, so even the last row needs room for three more than
+    it has (2560 elements: 13 groups of 8 bytes a row)."""
+    groups = -(-K // 256)
+    for M in (1, 9, 64, 200, 2048):
+        codes = M * groups * 128
+        assert Q.qgemm_workspace_size(M, K, 64, "mxfp4a4") >= codes + M * (groups + 3) * 8
+
+
 def test_row_conversion_refusals():
     lib = Q.load()
     quant = lambda R=2, K=64, t=0, x=A, ld=64, q=A, s=A: lib.qgemm_mx_quantize_device(R, K, t, x, ld, q, s, None)

@@ -537,6 +537,9 @@ qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_for
     if (st != QGEMM_OK) return st;
     if (S == 0 || N == 0 || a_rows == 0) return QGEMM_OK;
     if (!rows && a_rows < S) return QGEMM_ERR_SHAPE;
+    // gathered rows are addressed with 32-bit byte offsets
+    const size_t row_bytes = f == QGEMM_MXFP4_A4 ? round_up(K, 256) / 2 : (size_t)K * 2;
+    if (rows && (size_t)a_rows * row_bytes > 0xFFFFFFFFu) return QGEMM_ERR_SHAPE;
     if (!A || !offsets || !Bq || !scales || !C) return QGEMM_ERR_NULL;
     if (!aligned16(A) || !aligned16(offsets) || (rows && !aligned16(rows)) || !aligned16(Bq) || !aligned16(scales) ||
         !aligned16(C))

@@ -25,6 +25,9 @@ constexpr int kMaxDim = 1 << 24;
 // W4A8 keeps D = sum_k qa * q in int32: |D| <= K * 127 * 15 must stay < 2^31.
 constexpr long long kW4A8MaxK = ((1LL << 31) - 1) / (127 * 15);
 
+// The MXFP4 products address a tile's rows of A with 32-bit byte offsets.
+constexpr int kMxMaxK = 1 << 22;
+
 // The quantised formats carry [offset, scale] pairs; float weights do not, and
 // the MXFP4 formats carry scale bytes.
 static bool has_pairs(qgemm_format f) { return f != QGEMM_F32 && f != QGEMM_F16 && !is_mx(f); }
@@ -89,7 +92,7 @@ qgemm_status geometry(int K, int N, qgemm_format f, Geometry *g) {
         break;
     case QGEMM_MXFP4:
     case QGEMM_MXFP4_A4:
-        if (K == 0 || K % 64 != 0) return QGEMM_ERR_SHAPE;
+        if (K == 0 || K % 64 != 0 || K > kMxMaxK) return QGEMM_ERR_SHAPE;
         r.Kp = K; r.Np = (int)round_up(N, 32); r.nblk = K / 32; r.block = 32;
         r.w_bytes = round_up((size_t)(r.Np / 32) * (K / 64) * 1024, kPackAlign);
         r.s_bytes = (size_t)(r.Np / 32) * (round_up(K, 256) / 256) * 256;
@@ -126,13 +129,13 @@ MxWorkspace mx_workspace(qgemm_format f, long long rows, int K) {
     if (f != QGEMM_MXFP4_A4) return w;
     const size_t n256 = round_up(K, 256) / 256;
     w.s_off = round_up((size_t)rows * n256 * 128, kPackAlign);
-    w.bytes = w.s_off + round_up((size_t)rows * n256 * 8, kPackAlign);
+    w.bytes = w.s_off + round_up((size_t)rows * mx_act_groups((unsigned)n256) * 8, kPackAlign);
     return w;
 }
 
 long long mx_grid(int S, int E, int N) {
     const long long groups = E < S ? E : S;
-    return (groups + (S - groups) / 32) * div_up(N, 128);
+    return (groups + (S - groups) / 32) * div_up(N, 32) + 7;
 }
 
 int f32_kgroups(int M, int N) {

@@ -44,50 +44,86 @@ __device__ __forceinline__ unsigned mx_encode8(const float (&v)[8], unsigned top
 
 // ---------------------------------------------------------------------------
 // Groups of rows. A product's slots [0, S) fall into E consecutive groups
-// (offsets[0 .. E]); a row tile holds up to BM slots of one group, and the
-// tiles are numbered through all groups. offsets == nullptr: one group of all
-// S rows. Every offset is limited to [0, S], whatever the array holds.
+// (offsets[0 .. E]); a row tile holds up to BM slots of one group. offsets ==
+// nullptr: one group of all S rows. Every offset is limited to [0, S],
+// whatever the array holds.
+//
+// Order of the output tiles: group by group; within a group by bands of up to
+// kBand row tiles, in a band column by column, the band's row tiles of one
+// column in a row. The hardware deals workgroups to the eight XCDs in turn,
+// and each XCD has its own L2; XCD x takes the x-th eighth of that order, so
+// the workgroups that run on it together read the same few weight columns and
+// the same rows, and each weight is fetched by one XCD. (The eighths are of
+// the tiles that exist, which only the GPU knows.) Measured against plain
+// order with MXFP4 activations: 2048 x 4096 x 11008 in 64 x 256 tiles 134 ->
+// 102 us; bands of 1, 4 and 16: 128, 105, 101 us there, and 4096^3 with fp16
+// activations 120, 117, 120 us.
 // ---------------------------------------------------------------------------
 struct RowTile {
-    int e;        // group; -1 past the last tile
+    int e;        // group; -1: nothing to do
     int s0, n;    // first slot and number of slots
+    int tn;       // column tile
 };
 
-// Row tile `tile`, found by the whole wave (every wave of a workgroup does so
-// for itself): each lane counts one group's tiles, a scan over the lanes adds
-// them up, 64 groups at a time.
-__device__ __forceinline__ RowTile find_row_tile(const int32_t *__restrict__ offsets, int E, int S, int BM,
-                                                 int tile) {
+constexpr int kBand = 4;
+
+// Tile i of a group of slots [lo, hi), as above.
+__device__ __forceinline__ RowTile tile_of_group(int e, int lo, int hi, int BM, int tiles_n, int i) {
+    const int cnt = (hi - lo + BM - 1) / BM;
+    const int band = i / (kBand * tiles_n), rest = i - band * (kBand * tiles_n);
+    const int rows = min(kBand, cnt - band * kBand);
+    const int tn = rest / rows, s0 = lo + (band * kBand + rest - tn * rows) * BM;
+    return RowTile{e, s0, min(BM, hi - s0), tn};
+}
+
+// The tile of workgroup L of a launch of 8 * per-XCD workgroups, found by the
+// whole wave (every wave of a workgroup does so for itself): each lane counts
+// one group's row tiles, a scan over the lanes adds them up, 64 groups at a
+// time.
+__device__ __forceinline__ RowTile find_tile(const int32_t *__restrict__ offsets, int E, int S, int BM, int tiles_n,
+                                             int L) {
+        const int x = L & 7, idx = L >> 3;
     if (!offsets) {
-        const int s0 = tile * BM;
-        return s0 < S ? RowTile{0, s0, min(BM, S - s0)} : RowTile{-1, 0, 0};
+        const int total = (S + BM - 1) / BM * tiles_n, per = (total + 7) >> 3, q = x * per + idx;
+        return idx < per && q < total ? tile_of_group(0, 0, S, BM, tiles_n, q) : RowTile{-1, 0, 0, 0};
     }
     const int lane = threadIdx.x & 63;
-    int before = 0;                       // tiles of the groups already passed
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
+    auto bounds = [&](int e, int *lo, int *hi) {
+        *lo = *hi = 0;
         if (e < E) {
-            lo = min(max(offsets[e], 0), S);
-            hi = min(max(offsets[e + 1], lo), S);
+            *lo = min(max(offsets[e], 0), S);
+            *hi = min(max(offsets[e + 1], *lo), S);
         }
+    };
+    int lo, hi, all = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        bounds(e0 + lane, &lo, &hi);
+        all += (hi - lo + BM - 1) / BM;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
+    const int total = all * tiles_n, per = (total + 7) >> 3, q = x * per + idx;
+    if (idx >= per || q >= total) return RowTile{-1, 0, 0, 0};
+    int before = 0;                       // row tiles of the groups already passed
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        if (E > 64) bounds(e0 + lane, &lo, &hi);
         const int nt = (hi - lo + BM - 1) / BM;
         int upto = nt;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int x = __shfl_up(upto, d);
-            if (lane >= d) upto += x;
+            const int y = __shfl_up(upto, d);
+            if (lane >= d) upto += y;
         }
-        const unsigned long long past = __ballot(before + upto > tile);
+        const unsigned long long past = __ballot((before + upto) * tiles_n > q);
         if (past) {
             const int src = __ffsll((long long)past) - 1;
-            const int first = before + __shfl(upto - nt, src);     // tiles before group src
-            const int s0 = __shfl(lo, src) + (tile - first) * BM;
-            return RowTile{uniform(e0 + src), uniform(s0), uniform(min(BM, __shfl(hi, src) - s0))};
+            const int first = uniform(before + __shfl(upto - nt, src));     // row tiles before group src
+            return tile_of_group(uniform(e0 + src), uniform(__shfl(lo, src)), uniform(__shfl(hi, src)), BM, tiles_n,
+                                 q - first * tiles_n);
         }
         before += __shfl(upto, 63);
     }
-    return RowTile{-1, 0, 0};
+    return RowTile{-1, 0, 0, 0};
 }
 
 }  // namespace qg

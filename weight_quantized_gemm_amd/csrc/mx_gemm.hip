@@ -25,74 +25,594 @@ __device__ __forceinline__ i8v_t mx_operand(u4_t c) {
 
 constexpr int kFp4 = 4;      // operand type of the scaled MFMA
 
-__device__ __forceinline__ f16_t mfma_fp4(u4_t a, u4_t b, f16_t c, unsigned sa, unsigned sb) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, kFp4, kFp4, 0,
-                                                           (int)sa, 0, (int)sb);
+// c += a x b with byte s (a constant once unrolled) of the scale words.
+__device__ __forceinline__ f16_t mfma_fp4(u4_t a, u4_t b, f16_t c, unsigned sa, unsigned sb, int s) {
+#define QG_MFMA(S)                                                                                         \
+    __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, kFp4, kFp4, S, (int)sa, \
+                                                    S, (int)sb)
+    switch (s) {
+    case 0: return QG_MFMA(0);
+    case 1: return QG_MFMA(1);
+    case 2: return QG_MFMA(2);
+    default: return QG_MFMA(3);
+    }
+#undef QG_MFMA
 }
 
-// One wave per 32 x 32 tile of C, operands straight from memory.
-template <bool A4>
-__global__ __launch_bounds__(256) void mx_gemm_kernel(MxArgs p) {
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5;
-    const int tile_m = blockIdx.x / p.tiles_n, tn = blockIdx.x % p.tiles_n;
-    const RowTile rt = find_row_tile(p.offsets, p.E, p.S, 32, tile_m);
-    if (rt.e < 0) return;
-    const int n64 = p.K >> 6, n256 = (p.K + 255) >> 8;
-    const int t = min(tn * 4 + wave, (p.N + 31) / 32 - 1);
-    const uint8_t *W = p.W + (size_t)rt.e * p.w_bytes + (size_t)t * n64 * 1024 + lane * 16;
-    const uint8_t *Ws = p.Ws + (size_t)rt.e * p.s_bytes + (size_t)t * n256 * 256 + lane * 4;
-    const int slot = rt.s0 + min(r, rt.n - 1);
-    const size_t arow = p.rows ? (size_t)min(max(p.rows[slot], 0), p.a_rows - 1) : (size_t)slot;
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, void *lds, unsigned voff, unsigned soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, (int)voff,
+                                             (int)soff, 0, 0);
+#endif
+}
+__device__ __forceinline__ u4_t load16(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
+    return __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
+}
+__device__ __forceinline__ unsigned load4(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
+    return __builtin_bit_cast(unsigned, __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0));
+}
+__device__ __forceinline__ unsigned load1(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
+    return __builtin_amdgcn_raw_buffer_load_b8(r, (int)voff, (int)soff, 0);
+}
 
-    f16_t acc = {};
-    if constexpr (A4) {
-        const uint8_t *a = p.Aq + arow * n256 * 128 + 16 * h;
-        const uint8_t *as = p.As + (arow * n256 * 2 + h) * 4;
-        for (int b = 0; b < n64; ++b)
-            acc = mfma_fp4(*reinterpret_cast<const u4_t *>(a + 32 * b),
-                           *reinterpret_cast<const u4_t *>(W + (size_t)b * 1024), acc,
-                           as[(b >> 2) * 8 + (b & 3)], Ws[(b >> 2) * 256 + (b & 3)]);
-    } else {
-        const _Float16 *a = static_cast<const _Float16 *>(p.A) + arow * p.K + 32 * h;
-        for (int b = 0; b < n64; ++b) {
-            const u4_t w = *reinterpret_cast<const u4_t *>(W + (size_t)b * 1024);
-            const float s = mx_scale(Ws[(b >> 2) * 256 + (b & 3)]);
+// A's row of a slot: through the index, limited to A's rows, or the slot.
+__device__ __forceinline__ int a_row(const MxArgs &p, int slot) {
+    return p.rows ? min(max(p.rows[slot], 0), p.a_rows - 1) : slot;
+}
+
+// A workgroup barrier without __syncthreads' release fence, which would also
+// wait for the loads in flight; LDS reads before it have been consumed, and
+// the fence keeps later ones behind it.
+__device__ __forceinline__ void stage_barrier() {
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
+// Orders one wave's LDS writes before its later reads of them (and the other
+// way round) for the compiler; the hardware keeps a wave's LDS operations in
+// order.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The library's activations. SiLU x / (1 + e^-x) without the full-range
+// exponential and division, which cost more than the rest of a prefill
+// epilogue (2048 x 11008 outputs: 24 us of vector instructions against 6):
+// e^-x = 2^t (1 + c) with t = -x log2 e in one rounding and c its error times
+// ln 2 (two fused multiply-adds, log2 e in two parts), so the hardware's
+// 2^t and 1 / d leave about two units. x is limited to [-88.5, 100] in the
+// exponent, where the result is x or below 1e-36 in size.
+// For an fp16 result the first rounding alone (a few 2^-24 of the value) is
+// far below the result's own.
+__device__ __forceinline__ float silu16(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269502f));
+}
+__device__ __forceinline__ float silu32(float v) {
+    const float x = __builtin_amdgcn_fmed3f(v, -88.5f, 100.0f);
+    const float t = x * -1.44269502f;                             // log2 e = 1.44269502 + 1.92596303e-8
+    const float c = fmaf(x, -1.92596303e-8f, fmaf(x, -1.44269502f, -t));
+    float p = __builtin_amdgcn_exp2f(t);
+    p = fmaf(p, c * 0.693147181f, p);
+    return v * __builtin_amdgcn_rcpf(1.0f + p);
+}
+
+// The epilogue of a lane that holds columns n .. n + 3 (n a multiple of 4) of
+// several rows: its bias is loaded once, rows are handled B at a time with
+// every load of a batch requested before the first use.
+struct ColumnEpilogue {
+    Epilogue epi;
+    void *C;
+    int n, N;
+    f4_t bias;
+
+    __device__ __forceinline__ ColumnEpilogue(const Epilogue &e, void *C_, int n_, int N_)
+        : epi(e), C(C_), n(n_), N(N_), bias{0.f, 0.f, 0.f, 0.f} {
+        if (!e.bias) return;
+        if ((N & 3) == 0) {
+            if (n < N) bias = *reinterpret_cast<const f4_t *>(e.bias + n);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                    *reinterpret_cast<const h8_t *>(a + 64 * b + 8 * i), mx_decode8(w[i], s), acc, 0, 0, 0);
+                if (n + i < N) bias[i] = e.bias[n + i];
         }
     }
-    const int n = (tn * 4 + wave) * 32 + r;
-    if (n >= p.N) return;
+
+    template <int B>
+    __device__ __forceinline__ void activate(f4_t (&v)[B]) const {
+        if (epi.act == QGEMM_ACT_NONE) return;
+        if (epi.act == QGEMM_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[i][c] = epi.f16 ? silu16(v[i][c]) : silu32(v[i][c]);
+        } else if (epi.act == QGEMM_ACT_RELU) {
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[i][c] = v[i][c] > 0.f ? v[i][c] : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const float x = epi_act(v[i][0], QGEMM_ACT_GELU);
+                    v[i] = f4_t{v[i][1], v[i][2], v[i][3], x};
+                }
+        }
+    }
+
+    // rows m, m + step, ... (those below `rows`), with values v
+    template <int B>
+    __device__ __forceinline__ void put(size_t slot0, int m, int step, int rows, f4_t (&v)[B]) const {
+        if (n >= N) return;
+        if ((N & 3) == 0) {
+            if (epi.residual) {
+                f4_t res[B];
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    // (a row past the end re-reads the last one, to keep the loads together)
+                    const size_t mn = (slot0 + min(m + i * step, rows - 1)) * N + n;
+                    if (epi.f16) {
+                        const h4_t x = *reinterpret_cast<const h4_t *>(static_cast<const _Float16 *>(epi.residual) + mn);
+                        res[i] = f4_t{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+                    } else {
+                        res[i] = *reinterpret_cast<const f4_t *>(static_cast<const float *>(epi.residual) + mn);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) v[i] = (v[i] + bias) + res[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < B; ++i) v[i] = v[i] + bias;
+            }
+            activate(v);
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (m + i * step >= rows) return;
+                const size_t mn = (slot0 + m + i * step) * N + n;
+                if (epi.f16)
+                    *reinterpret_cast<h4_t *>(static_cast<_Float16 *>(C) + mn) =
+                        h4_t{(_Float16)v[i][0], (_Float16)v[i][1], (_Float16)v[i][2], (_Float16)v[i][3]};
+                else
+                    *reinterpret_cast<f4_t *>(static_cast<float *>(C) + mn) = v[i];
+            }
+        } else {
+            // rows of C (and of bias and residual) start at any column
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const size_t mn = (slot0 + min(m + i * step, rows - 1)) * N + n;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    v[i][c] += bias[c];
+                    if (epi.residual && n + c < N)
+                        v[i][c] += epi.f16 ? (float)static_cast<const _Float16 *>(epi.residual)[mn + c]
+                                           : static_cast<const float *>(epi.residual)[mn + c];
+                }
+            }
+            activate(v);
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (m + i * step >= rows) return;
+                const size_t mn = (slot0 + m + i * step) * N + n;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n + c < N) epi_store(epi, C, mn + c, v[i][c]);
+            }
+        }
+    }
+};
+
+// s_waitcnt operand: at most n vector memory loads outstanding, and no LDS read.
+constexpr int stage_wait(int n) { return vm_wait(n) & ~0xF00; }
+
+// ---------------------------------------------------------------------------
+// Tiled product
+// ---------------------------------------------------------------------------
+template <bool A4_, int RF_, int CF_, int WM_, int WN_, int WK_, int NS_, int BR_, int MINW_ = 1>
+struct Tile {
+    static constexpr bool A4 = A4_;
+    static constexpr int RF = RF_, CF = CF_, WM = WM_, WN = WN_, WK = WK_, NS = NS_, BR = BR_, MINW = MINW_;
+    static constexpr int BM = 32 * RF * WM, BN = 32 * CF * WN;
+    static constexpr int GW = WM * WN;                    // waves of a K group
+    static constexpr int THREADS = 64 * GW * WK;
+    static constexpr int SLOT = BM * 128;                 // bytes of A per stage
+    static constexpr int D = BM / 8 / GW;                 // DMA instructions per wave and stage
+    static constexpr int NREC = A4 ? 4 : 1;               // weight records per stage and column fragment
+    static constexpr int NB = CF * NREC + CF;             // other loads per wave and stage
+    // scales of the tile's rows (MXFP4 activations): 8 bytes a stage, the NS
+    // stages of an unrolled turn in one of two slots; in DMA instructions of
+    // RPI rows
+    static constexpr int PPR = NS / 2;                    // 16-byte pieces per row
+    static constexpr int RPI = 64 / PPR;
+    static constexpr int ASC = A4 ? (BM + RPI - 1) / RPI * 1024 : 0;          // bytes of a slot
+    static constexpr int DS = A4 ? (BM / RPI + GW - 1) / GW : 0;
+    static constexpr int SR = A4 ? 2 : BR;                // register slots of the scales
+    // loads issued since the DMA of the next stage when a wave waits for it
+    // (the weights' and scales' of that stage, everything of NS - 2 more)
+    static constexpr int WAIT = NB + (NS - 2) * (D + NB);
+    // loads issued after the prologue's DMA
+    static constexpr int PRO = A4 ? BR * 4 * CF + 2 * CF : BR * NB;
+    // floats per row of a wave's C block in LDS: rows 4 apart, which one
+    // instruction writes, fall into different halves of the banks
+    static constexpr int PITCH = 32 * CF + 8;
+    static constexpr int LDS_A = WK * (NS * SLOT + 2 * ASC);
+    static constexpr int LDS_C = WK > 1 ? WK * BM * BN * 4 : GW * 32 * PITCH * 4;
+    static constexpr int LDS = LDS_A > LDS_C ? LDS_A : LDS_C;
+    static_assert(D * 8 * GW == BM, "whole DMA instructions");
+    static_assert(!A4 || NS == 2 || NS == 4, "whole pieces of scales");
+    static_assert(NS % SR == 0 && NS % BR == 0, "register slots repeat within an unrolled turn");
+    static_assert(WAIT <= 63 && PRO <= 63, "vmcnt range");
+    static_assert(LDS <= 160 * 1024, "LDS of a workgroup");
+};
+
+template <class T>
+__global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) {
+    constexpr bool A4 = T::A4;
+    constexpr int RF = T::RF, CF = T::CF, NS = T::NS, BR = T::BR, D = T::D, WK = T::WK;
+    __shared__ __align__(16) unsigned char lds[T::LDS];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5;
+    const int kg = wave / T::GW, gw = wave % T::GW, wm = gw / T::WN, wn = gw % T::WN;
+    RowTile rt = find_tile(p.offsets, p.E, p.S, T::BM, p.tiles_n, blockIdx.x);
+    if (rt.e < 0) return;
+    // scalars: the buffer resources built from them must be
+    rt = RowTile{uniform(rt.e), uniform(rt.s0), uniform(rt.n), uniform(rt.tn)};
+    const int tn = rt.tn;
+    const int n64 = p.K >> 6, n256 = (p.K + 255) >> 8;
+    // this K group's stages
+    const int nall = A4 ? n256 : n64;
+    // (of whole pairs with MXFP4 activations, whose scales come in pairs)
+    constexpr int U = A4 ? 2 : 1;
+    const int units = (nall + U - 1) / U;
+    const int st0 = U * (kg * units / WK), nst = min(U * ((kg + 1) * units / WK), nall) - st0;
+    const int nmax = U * ((units + WK - 1) / WK);      // of the longest K group, at most
+    const int last = max(nst - 1, 0);
+
+    // A: gathered rows from the array's start, others from the tile's first row
+    const unsigned row_bytes = A4 ? (unsigned)n256 * 128u : (unsigned)p.K * 2u;
+    const size_t first = p.rows ? 0 : (size_t)rt.s0;
+    const uint8_t *Ab = (A4 ? p.Aq : static_cast<const uint8_t *>(p.A)) + first * row_bytes;
+    const __amdgpu_buffer_rsrc_t a_rs = byte_rsrc(Ab, 0xFFFFFFFFu);
+    unsigned a_off[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+        const int row = 8 * (gw + T::GW * i) + (lane >> 3);
+        a_off[i] = (unsigned)(a_row(p, rt.s0 + min(row, rt.n - 1)) - (int)first) * row_bytes +
+                   16u * ((lane & 7) ^ (lane >> 3));
+    }
+    // scales: 16-byte piece x (two stages) of a row stands at x ^ (row / 8 %
+    // 2), so that the 32 rows one instruction reads spread over the banks;
+    // lane l of an instruction brings piece l % PPR of row l / PPR
+    const unsigned as_bytes = mx_act_groups(n256) * 8u;
+    const __amdgpu_buffer_rsrc_t as_rs = byte_rsrc(A4 ? p.As + first * as_bytes : p.As, 0xFFFFFFFFu);
+    unsigned as_off[A4 ? T::DS : 1];
+    if constexpr (A4) {
+#pragma unroll
+        for (int i = 0; i < T::DS; ++i) {
+            const int row = min(T::RPI * (gw + T::GW * i) + lane / T::PPR, T::BM - 1);
+            as_off[i] = (unsigned)(a_row(p, rt.s0 + min(row, rt.n - 1)) - (int)first) * as_bytes +
+                        16u * (T::PPR == 1 ? 0u : (lane ^ (row >> 3)) & 1u);
+        }
+    }
+    // B: the records and scales of this wave's column fragments
+    const int ntiles = (p.N + 31) / 32;
+    __amdgpu_buffer_rsrc_t b_rs[CF], bs_rs[CF];
+#pragma unroll
+    for (int cf = 0; cf < CF; ++cf) {
+        const int t = min((tn * T::WN + wn) * CF + cf, ntiles - 1);
+        b_rs[cf] = byte_rsrc(p.W + (size_t)rt.e * p.w_bytes + (size_t)t * n64 * 1024, (unsigned)n64 * 1024u);
+        bs_rs[cf] = byte_rsrc(p.Ws + (size_t)rt.e * p.s_bytes + (size_t)t * n256 * 256, (unsigned)n256 * 256u);
+    }
+
+    unsigned char *const mine = lds + (size_t)kg * (NS * T::SLOT + 2 * T::ASC);
+    unsigned char *const mine_s = mine + NS * T::SLOT;
+    auto dma = [&](int slot, int st) {
+        const unsigned so = (unsigned)(st0 + min(st, last)) * 128u;
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+            dma16(a_rs, mine + slot * T::SLOT + (gw + T::GW * i) * 1024, a_off[i], so);
+    };
+    // the scales of turn c (stages NS c ..) into slot c % 2
+    auto dma_scales = [&](int c) {
+        const unsigned so = (unsigned)(st0 + min(NS * c, last / NS * NS)) * 8u;
+#pragma unroll
+        for (int i = 0; i < T::DS; ++i)
+            if (T::DS * T::GW * T::RPI == T::BM || T::RPI * (gw + T::GW * i) < T::BM)
+                dma16(as_rs, mine_s + (c & 1) * T::ASC + (gw + T::GW * i) * 1024, as_off[i], so);
+    };
+    // MXFP4 activations: a record per step, reloaded for the next stage as
+    // soon as its step has run, and the stage's scale words in two slots.
+    // fp16 activations: one record and scale byte for the whole stage.
+    u4_t bc[BR][CF][T::NREC];
+    unsigned bs[T::SR][CF], as[T::SR][RF];
+    auto load_codes = [&](int j, int rec, int st) {
+        const int k = (st0 + min(st, last)) * T::NREC + rec;
+#pragma unroll
+        for (int cf = 0; cf < CF; ++cf)
+            bc[j][cf][rec] = load16(b_rs[cf], lane * 16u, (unsigned)min(k, n64 - 1) * 1024u);
+    };
+    auto load_scales = [&](int j, int st) {
+        const int k = st0 + min(st, last);
+#pragma unroll
+        for (int cf = 0; cf < CF; ++cf)
+            bs[j][cf] = A4 ? load4(bs_rs[cf], lane * 4u, (unsigned)k * 256u)
+                           : load1(bs_rs[cf], lane * 4u, (unsigned)(k >> 2) * 256u + (k & 3));
+    };
+    // the words of a turn's stage u
+    auto read_scales = [&](int j, int c, int u) {
+        if constexpr (A4) {
+            const unsigned char *src = mine_s + (c & 1) * T::ASC + (32 * RF * wm + r) * (16 * T::PPR) +
+                                       16 * (T::PPR == 1 ? 0 : (u >> 1 ^ r >> 3) & 1) + 8 * (u & 1) + 4 * h;
+#pragma unroll
+            for (int rf = 0; rf < RF; ++rf)
+                as[j][rf] = *reinterpret_cast<const unsigned *>(src + rf * 32 * (16 * T::PPR));
+        }
+    };
+
+    f16_t acc[RF][CF];
+#pragma unroll
+    for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int j = 0; j < CF; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+    // operands of one MFMA step: s of the stage in LDS slot `slot` and register slot j
+    u4_t a[2][RF];
+    h8_t b[2][CF];
+    const unsigned char *const a_lds = mine + (32 * RF * wm + r) * 128;
+    auto read_a = [&](u4_t (&dst)[RF], int slot, int s) {
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf)
+            dst[rf] = *reinterpret_cast<const u4_t *>(a_lds + slot * T::SLOT + rf * 4096 +
+                                                      16 * ((A4 ? 2 * s + h : 4 * h + s) ^ (r & 7)));
+    };
+    auto decode_b = [&](h8_t (&dst)[CF], int j, int s) {
+        if constexpr (!A4) {
+#pragma unroll
+            for (int cf = 0; cf < CF; ++cf) {
+                dst[cf] = mx_decode8(bc[j][cf][0][s], mx_scale(bs[j % T::SR][cf]));
+                asm volatile("" : "+v"(dst[cf]));      // formed here, not next to its use
+            }
+        }
+    };
+    auto multiply = [&](int x, int j, int y, int s) {
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf)
+#pragma unroll
+            for (int cf = 0; cf < CF; ++cf) {
+                if constexpr (A4)
+                    acc[rf][cf] = mfma_fp4(a[x][rf], bc[y][cf][s], acc[rf][cf], as[j][rf], bs[j][cf], s);
+                else
+                    acc[rf][cf] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, a[x][rf]), b[x][cf],
+                                                                         acc[rf][cf], 0, 0, 0);
+            }
+        if constexpr (A4) {
+#pragma unroll
+            for (int i = 0; i < RF; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, CF, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RF; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+            for (int i = 0; i < RF * CF; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, (6 + RF - 1) / RF, 0);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    if constexpr (A4) dma_scales(0);
+#pragma unroll
+    for (int d = 0; d < NS; ++d) dma(d, d);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < T::SR || d < BR; ++d) {
+        if (d < BR) {
+#pragma unroll
+            for (int k = 0; k < T::NREC; ++k) load_codes(d, k, d);
+        }
+        if (d < T::SR) load_scales(d, d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(vm_wait(T::PRO));
+    stage_barrier();
+    read_scales(0, 0, 0);
+    read_a(a[0], 0, 0);
+    decode_b(b[0], 0, 0);
+
+    for (int base = 0; base < nst; base += NS) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const int i = base + u;
+            if (u > 0 && i >= nst) break;          // wave-uniform
+            const int j = u % T::SR, y = u % BR;
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+                read_a(a[(s + 1) & 1], u, s + 1);
+                decode_b(b[(s + 1) & 1], j, s + 1);
+                multiply(s & 1, j, y, s);
+                if constexpr (A4) {
+                    load_codes(y, s, i + BR);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            // (no branch here: the optimiser would move the matrix
+            // instructions above into the block behind it, past the loads)
+            __builtin_amdgcn_s_waitcnt(stage_wait(T::WAIT));
+            stage_barrier();
+            dma(u, i + NS);
+            // (the other slot's scales, of the turn before, have been read)
+            if constexpr (A4) {
+                if (u == 0) dma_scales(base / NS + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            read_scales((u + 1) % T::SR, base / NS + (u + 1) / NS, (u + 1) % NS);
+            read_a(a[0], (u + 1) % NS, 0);
+            if constexpr (!A4) {
+                load_codes(j, 0, i + BR);
+                load_scales(j, i + BR);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            decode_b(b[0], (u + 1) % T::SR, 0);
+            multiply(1, j, y, 3);
+            if constexpr (A4) {
+                load_codes(y, 3, i + BR);
+                load_scales(j, i + 2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+
+    // every wave of the workgroup meets as many barriers
+    if constexpr (WK > 1) {
+        for (int i = nst; i < nmax; ++i) stage_barrier();
+    }
+
+    // ---- C goes through LDS so that a lane holds four neighbouring columns
+    //      of a row: whole vectors of bias, residual and C, and the epilogue's
+    //      code once, in rolled loops (written out per accumulator register
+    //      it left the instruction cache and waited for each bias load) ----
     Epilogue epi = p.epi;
     if (epi.bias) epi.bias += (size_t)rt.e * p.N;
+    const int n0 = tn * T::BN;
+    __builtin_amdgcn_s_waitcnt(vm_wait(0));      // no DMA in flight into what follows
+    __syncthreads();
+    float *const out = reinterpret_cast<float *>(lds);
+    if constexpr (WK > 1) {
+        // the K groups' partial tiles, added in the order of K
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int m = 8 * (j >> 2) + 4 * h + (j & 3);
-        if (m < rt.n) epi_put(epi, p.C, rt.s0 + m, n, p.N, acc[j]);
+        for (int rf = 0; rf < RF; ++rf)
+#pragma unroll
+            for (int cf = 0; cf < CF; ++cf)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    out[(kg * T::BM + 32 * (RF * wm + rf) + 8 * (j >> 2) + 4 * h + (j & 3)) * T::BN +
+                        32 * (CF * wn + cf) + r] = acc[rf][cf][j];
+        __syncthreads();
+        constexpr int TPR = T::BN / 4, STEP = T::THREADS / TPR;      // threads per row, rows per turn
+        static_assert(T::THREADS % TPR == 0, "a thread keeps its columns");
+        const int col = 4 * (threadIdx.x % TPR);
+        const ColumnEpilogue ce(epi, p.C, n0 + col, p.N);
+        const float *src = out + (threadIdx.x / TPR) * T::BN + col;
+#pragma unroll 1
+        for (int m = threadIdx.x / TPR; m < rt.n; m += STEP, src += STEP * T::BN) {
+            f4_t v[1] = {*reinterpret_cast<const f4_t *>(src)};
+#pragma unroll
+            for (int g = 1; g < WK; ++g) v[0] += *reinterpret_cast<const f4_t *>(src + g * T::BM * T::BN);
+            ce.put(rt.s0, m, STEP, rt.n, v);
+        }
+    } else {
+        // each wave by itself, 32 rows of its columns at a time
+        float *const own = out + wave * 32 * T::PITCH;
+        constexpr int LPR = 8 * CF, STEP = 64 / LPR;      // lanes per row, rows per turn
+        const int col = 4 * (lane % LPR);
+        const ColumnEpilogue ce(epi, p.C, n0 + 32 * CF * wn + col, p.N);
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf) {
+            const int m0 = 32 * (RF * wm + rf);
+            if (m0 >= rt.n) break;               // wave-uniform
+#pragma unroll
+            for (int cf = 0; cf < CF; ++cf)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    own[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * cf + r] = acc[rf][cf][j];
+            wave_lds_sync();
+#pragma unroll 1
+            for (int m = lane / LPR; m < 32; m += 4 * STEP) {
+                f4_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = *reinterpret_cast<const f4_t *>(own + (m + i * STEP) * T::PITCH + col);
+                if (m0 + m < rt.n) ce.put(rt.s0, m0 + m, STEP, rt.n, v);
+            }
+            wave_lds_sync();
+        }
     }
 }
 
 }  // namespace
 
+namespace {
+// The most row tiles of `rows` rows that S slots in `groups` groups can make.
+long long most_row_tiles(int S, long long groups, int rows) {
+    if (groups > S) groups = S;
+    return groups + (S - groups) / rows;
+}
+
+template <class T>
+hipError_t launch_tile(MxArgs p, hipStream_t s) {
+    p.tiles_n = div_up(p.N, T::BN);
+    const long long grid = most_row_tiles(p.S, p.offsets ? p.E : 1, T::BM) * p.tiles_n;
+    hipLaunchKernelGGL(mx_tile_kernel<T>, dim3((unsigned)((grid + 7) / 8 * 8)), dim3(T::THREADS), 0, s, p);
+    return hipGetLastError();
+}
+
+// Tile shapes, from large to small. Large tiles move fewer bytes into a CU for
+// each matrix instruction; small ones, and more K groups in a workgroup, keep
+// 256 CUs busy when C is small. Which one runs depends on how many tiles it
+// would make, from these measurements (us, MI355X, M x K x N; the tiles of
+// the shape in brackets):
+//   fp16 activations        128x256     64x256      64x128/2    32x64/4     32x32/8
+//   4096 x 4096 x 4096      115 [512]   121
+//   2048 x 4096 x 4096      69.9 [256]  64.0 [512]  74.9
+//   2048 x 9728 x 2560      125 [160]   115 [320]   116 [640]
+//   512 x 4096 x 4096       52.5        34.7 [128]  22.1 [256]  29.4
+//   128 x 2560 x 9728                   23.6        14.6 [152]  16.9 [608]
+//   128 x 4096 x 4096                               18.9 [64]   11.2 [256]  16.3
+//   8 x 2560 x 9728                                 12.8        8.2 [152]   12.5 [304]
+//   64 x 4096 x 4096                                            10.7 [128]  9.4 [256]
+//   MXFP4 activations
+//   2048 x 9728 x 2560      57.9 [160]  67.5        65.3
+//   512 x 4096 x 4096       23.6 [64]   17.7        14.5 [256]
+// (the 128 x 256 tile's stages take twice as long with fp16 activations, so
+// a second round of them costs more there).
+enum Shape { T128x256, T64x256, T64x128, T32x64, T32x32 };
+constexpr int kTileRows[] = {128, 64, 64, 32, 32}, kTileCols[] = {256, 256, 128, 64, 32};
+
+Shape choose_shape(bool A4, int S, long long groups, int N) {
+    // row tiles to expect: the groups' last tiles are half empty on average
+    auto tiles = [&](Shape t) {
+        const int bm = kTileRows[t];
+        const long long full = groups <= 1 ? (S + bm - 1) / bm : S / bm + (groups < S ? groups : S) / 2;
+        return full * div_up(N, kTileCols[t]);
+    };
+    // rows of the average group: a tile of twice that is mostly padding
+    const long long rows = S / (groups < S ? groups : S);
+    if (rows > (A4 ? 96 : 384) && tiles(T128x256) >= (A4 ? 144 : 512)) return T128x256;
+    if (rows > 48 && tiles(T64x256) >= 256) return T64x256;
+    if (rows > 32 && tiles(T64x128) >= 144) return T64x128;
+    return tiles(T32x64) >= 144 ? T32x64 : T32x32;
+}
+
+template <bool A4>
+hipError_t launch_product(const MxArgs &p, hipStream_t s) {
+    switch (choose_shape(A4, p.S, p.offsets ? p.E : 1, p.N)) {
+    //                                       RF CF WM WN WK NS BR waves a SIMD
+    case T128x256: return launch_tile<Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T64x256:  return launch_tile<Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T64x128:  return launch_tile<Tile<A4, 2, 1, 1, 4, 2, 4, 2, 2>>(p, s);
+    case T32x64:   return launch_tile<Tile<A4, 1, 1, 1, 2, 4, 4, 2, 2>>(p, s);
+    default:       return launch_tile<Tile<A4, 1, 1, 1, 1, 8, 4, 2, 1>>(p, s);
+    }
+}
+}  // namespace
+
 hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, void *ws, hipStream_t s) {
     MxArgs p = args;
-    p.tiles_n = div_up(p.N, 128);
-    const dim3 grid((unsigned)mx_grid(p.S, p.offsets ? p.E : 1, p.N));
-    if (f == QGEMM_MXFP4_A4) {
-        const MxWorkspace w = mx_workspace(f, p.a_rows, p.K);
-        uint8_t *base = static_cast<uint8_t *>(ws);
-        const hipError_t e = launch_mx_quantize_act(p.a_rows, p.K, p.A, base, base + w.s_off, s);
-        if (e != hipSuccess) return e;
-        p.Aq = base;
-        p.As = base + w.s_off;
-        hipLaunchKernelGGL(mx_gemm_kernel<true>, grid, dim3(256), 0, s, p);
-    } else {
-        hipLaunchKernelGGL(mx_gemm_kernel<false>, grid, dim3(256), 0, s, p);
-    }
-    return hipGetLastError();
+    if (f != QGEMM_MXFP4_A4) return launch_product<false>(p, s);
+    const MxWorkspace w = mx_workspace(f, p.a_rows, p.K);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    const hipError_t e = launch_mx_quantize_act(p.a_rows, p.K, p.A, base, base + w.s_off, s);
+    if (e != hipSuccess) return e;
+    p.Aq = base;
+    p.As = base + w.s_off;
+    return launch_product<true>(p, s);
 }
 
 }  // namespace qg

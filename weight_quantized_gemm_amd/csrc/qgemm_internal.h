@@ -272,14 +272,14 @@ int splitk_plan(qgemm_format f, int M, int K, int N);      // 1 = no split
 // 32-channel tiles split K over the workgroups of a tile.
 int gemv_split_plan(qgemm_format f, int M, int K, int N);
 
-// ---------------------------------------------------------------------------
-// MXFP4 and the operators of mixture-of-experts layers.
-// ---------------------------------------------------------------------------
-// Byte of block (32-element half h of 64-element block b) of row r in the
-// activation scales: [row][K / 256][h][4], so that lane (row, h) of a matrix
-// operand finds the scales of four consecutive 64-blocks in one word.
+// Activation scales of MXFP4_A4: [row][groups][h][4], one group (a word per
+// 32-element half h, a byte per 64-block) for every 256 K-elements. A kernel
+// reads four groups at once, from any group on, so a row has room for three
+// more than it needs (never used, but inside the buffer).
+__host__ __device__ inline unsigned mx_act_groups(unsigned n256) { return (n256 + 6) / 4 * 4; }
+// Byte of half h of 64-block b of row r.
 __host__ __device__ inline size_t mx_act_scale(size_t r, unsigned b, unsigned h, unsigned n256) {
-    return ((r * n256 + (b >> 2)) * 2 + h) * 4 + (b & 3);
+    return ((r * mx_act_groups(n256) + (b >> 2)) * 2 + h) * 4 + (b & 3);
 }
 
 // The same for channel n of a packed weight: 256-byte records (32-channel
@@ -300,7 +300,7 @@ struct MxArgs {
     Epilogue epi;
     // set by the launcher
     const uint8_t *Aq, *As;           // MXFP4_A4: activation codes [a_rows][Kp / 2] and
-                                      // scales [a_rows][Kp / 256][2][4], Kp = roundup(K, 256)
+                                      // scales (mx_act_scale), Kp = roundup(K, 256)
     int tiles_n;
 };
 // MXFP4_A4 scratch: the codes of `rows` rows, then their scales.
@@ -308,7 +308,7 @@ struct MxWorkspace {
     size_t q_off, s_off, bytes;
 };
 MxWorkspace mx_workspace(qgemm_format f, long long rows, int K);
-// Workgroups of the product's launch (at most 2^31 - 1 are allowed).
+// Workgroups of the product's launch, at most (2^31 - 1 are allowed).
 long long mx_grid(int S, int E, int N);
 hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, void *ws, hipStream_t s);
 
