@@ -128,18 +128,19 @@ static bool use_gemv(qgemm_format f, int M, int K, int N) {
 // plan, so a concurrent qgemm_set_gemv_max_m cannot make one call size its
 // scratch for one kernel and launch another.
 struct CallPlan {
-    bool gemv;
+    bool gemv, mx;
     RunWorkspace r;
     int nsplit() const { return gemv ? r.gemv_nsplit : r.nsplit; }
-    // Scratch bytes the call touches: the W4A8 or MXFP4_A4 activation codes first, then
+    // Scratch bytes the call touches: the W4A8 or MXFP4_A4 activation codes
+    // first (the MXFP4 decode kernel quantises its rows itself), then
     // (when the kernel splits K) the partial tiles. The size reported to
     // callers (run_workspace().bytes) is a function of the shape alone and
     // never smaller than this.
-    size_t used_bytes() const { return nsplit() <= 1 ? r.act_bytes : r.bytes; }
+    size_t used_bytes() const { return mx && gemv ? 0 : nsplit() <= 1 ? r.act_bytes : r.bytes; }
 };
 
 static CallPlan plan_call(qgemm_format f, int M, int K, int N) {
-    return CallPlan{use_gemv(f, M, K, N), run_workspace(f, M, K, N)};
+    return CallPlan{use_gemv(f, M, K, N), is_mx(f), run_workspace(f, M, K, N)};
 }
 
 static qgemm_status run_w4a8(int M, int K, int N, const CallPlan &p, const void *A,
@@ -196,7 +197,7 @@ static qgemm_status dispatch(int M, int K, int N, qgemm_format f, const Geometry
                                                  static_cast<const uint8_t *>(Bq),
                                                  static_cast<const uint8_t *>(scales), 0, 0, C, epi, nullptr,
                                                  nullptr, 0},
-                                       ws, s));
+                                       gemv, ws, s));
     default:
         break;
     }
@@ -547,7 +548,8 @@ qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_for
     Epilogue epi;
     st = make_epilogue(epilogue, &epi);
     if (st != QGEMM_OK) return st;
-    const size_t need = mx_workspace(f, a_rows, K).bytes;
+    const bool decode = mx_grouped_decode(S, E, N);
+    const size_t need = decode ? 0 : mx_workspace(f, a_rows, K).bytes;
     st = check_scratch(need, workspace, ws_bytes);
     if (st != QGEMM_OK) return st;
     st = check_device();
@@ -558,7 +560,7 @@ qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_for
                       static_cast<const uint8_t *>(Bq), static_cast<const uint8_t *>(scales), g.w_bytes, g.s_bytes,
                       C, epi, nullptr, nullptr, 0};
     return with_scratch(need, workspace, ws_bytes, s,
-                        [&](void *ws) { return launched(launch_mx_gemm(f, args, ws, s)); });
+                        [&](void *ws) { return launched(launch_mx_gemm(f, args, decode, ws, s)); });
 }
 
 qgemm_status qgemm_group_combine(int T, int topk, int N, int S, const void *Y, int y_type, const int32_t *slots,

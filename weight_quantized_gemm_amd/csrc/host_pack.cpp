@@ -135,7 +135,7 @@ MxWorkspace mx_workspace(qgemm_format f, long long rows, int K) {
 
 long long mx_grid(int S, int E, int N) {
     const long long groups = E < S ? E : S;
-    return (groups + (S - groups) / 32) * div_up(N, 32) + 7;
+    return (groups + (S - groups) / 8) * div_up(N, 32) + 7;
 }
 
 int f32_kgroups(int M, int N) {

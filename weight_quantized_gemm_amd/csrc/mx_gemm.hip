@@ -48,6 +48,10 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, void *lds, unsig
 __device__ __forceinline__ u4_t load16(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
     return __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
 }
+// The same, past the caches, for bytes that no other workgroup wants.
+__device__ __forceinline__ u4_t load16_once(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
+    return __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 2));
+}
 __device__ __forceinline__ unsigned load4(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff) {
     return __builtin_bit_cast(unsigned, __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0));
 }
@@ -536,12 +540,199 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (decode): a row tile of RT (2 or 8) rows against 32 channels and
+// all of K, for which the weights are the bytes that matter. Eight waves share
+// K in groups of 256 elements, taken in turn (one group: four 1 KiB weight
+// records, one 256-byte scale record, 512 bytes of every row), each group's
+// loads all requested at once. The rows go through LDS, wave by wave without
+// a barrier: fp16 as they are, or quantised to MXFP4 on the way (a 32-element
+// block is what four neighbouring lanes loaded, so no pass over A of its own
+// is needed). The matrix cores run 32 rows wide and the lanes past RT repeat
+// real rows: at 1 x 4096 x 11008 that is 1.2 us of matrix work spread over
+// the chip beside 4.7 us of memory. The waves' partial sums are added in wave
+// order. ONCE (the dense product, whose weights one workgroup reads): weight
+// loads past the caches.
+// Measured (us): 1 x 4096 x 11008 8.2 (12.7 in 32 x 64 tiles; 8.8 through the
+// caches; 8.7 with RT = 8; two groups at once 8.4; 16 waves 8.2, 4 waves 9.1),
+// 8 x 4096 x 11008 9.6 (12.9), 1 x 9728 x 2560 8.5 (16.5 in 32 x 32 tiles; 16
+// waves 7.6, but 10 experts-grouped rows go from 19 to 27), MXFP4 activations
+// 1 x 4096 x 11008 8.0 (11.2 with the separate quantiser and tiles).
+// ---------------------------------------------------------------------------
+constexpr int kDecodeWaves = 8;
+
+template <bool A4, int RT, bool ONCE>
+__global__ __launch_bounds__(64 * kDecodeWaves) void mx_decode_kernel(MxArgs p) {
+    constexpr int AL = RT / 2;                             // 16-byte loads of A per lane and group
+    constexpr int PITCH = A4 ? 144 : 528;                  // bytes per row in LDS (4 banks more than a power of two)
+    constexpr int GROUP = RT * PITCH + (A4 ? RT * 8 : 0);  // bytes of a group: the rows, then their scales
+    static_assert(GROUP % 16 == 0 && RT <= 8, "aligned groups; C in registers 0 .. 3");
+    __shared__ __align__(16) unsigned char rows_lds[kDecodeWaves * GROUP];
+    __shared__ __align__(16) float sums[kDecodeWaves * RT * 32];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5;
+    RowTile rt = find_tile(p.offsets, p.E, p.S, RT, p.tiles_n, blockIdx.x);
+    if (rt.e < 0) return;
+    rt = RowTile{uniform(rt.e), uniform(rt.s0), uniform(rt.n), uniform(rt.tn)};
+    const int n64 = p.K >> 6, n256 = (p.K + 255) >> 8;
+    const __amdgpu_buffer_rsrc_t b_rs =
+        byte_rsrc(p.W + (size_t)rt.e * p.w_bytes + (size_t)rt.tn * n64 * 1024, (unsigned)n64 * 1024u);
+    const __amdgpu_buffer_rsrc_t bs_rs =
+        byte_rsrc(p.Ws + (size_t)rt.e * p.s_bytes + (size_t)rt.tn * n256 * 256, (unsigned)n256 * 256u);
+    // this lane's rows of A: half a wave loads the 256 elements of one
+    const _Float16 *a_src[AL];
+#pragma unroll
+    for (int i = 0; i < AL; ++i)
+        a_src[i] = static_cast<const _Float16 *>(p.A) + (size_t)a_row(p, rt.s0 + min(2 * i + h, rt.n - 1)) * p.K;
+    unsigned char *const mine = rows_lds + wave * GROUP, *const mine_s = mine + RT * PITCH;
+
+    f16_t acc;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (int g = wave; g < n256; g += kDecodeWaves) {
+        h8_t a[AL];
+        u4_t w[4];
+        // elements past K (of the last group) re-read the row's first ones,
+        // for records that are not used
+        const int k = 256 * g + 8 * r < p.K ? 256 * g + 8 * r : 0;
+#pragma unroll
+        for (int i = 0; i < AL; ++i) a[i] = *reinterpret_cast<const h8_t *>(a_src[i] + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned at = (unsigned)min(4 * g + j, n64 - 1) * 1024u;
+            w[j] = ONCE ? load16_once(b_rs, lane * 16u, at) : load16(b_rs, lane * 16u, at);
+        }
+        const unsigned ws = load4(bs_rs, lane * 4u, (unsigned)g * 256u);
+#pragma unroll
+        for (int i = 0; i < AL; ++i) {
+            const int row = 2 * i + h;
+            if constexpr (A4) {
+                float v[8];
+                unsigned top = 0, byte = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = (float)a[i][e];
+                    top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+                }
+                *reinterpret_cast<unsigned *>(mine + row * PITCH + 4 * r) = mx_encode8(v, top, &byte);
+                // block r / 4 of the eight: half r / 4 % 2 of 64-block r / 8
+                if ((r & 3) == 0) mine_s[row * 8 + 4 * (r >> 2 & 1) + (r >> 3)] = (uint8_t)byte;
+            } else {
+                *reinterpret_cast<h8_t *>(mine + row * PITCH + 16 * r) = a[i];
+            }
+        }
+        wave_lds_sync();
+        const unsigned char *const src = mine + (r % RT) * PITCH;
+        const unsigned as = A4 ? *reinterpret_cast<const unsigned *>(mine_s + (r % RT) * 8 + 4 * h) : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (4 * g + j >= n64) break;                   // wave-uniform
+            if constexpr (A4) {
+                acc = mfma_fp4(*reinterpret_cast<const u4_t *>(src + 32 * j + 16 * h), w[j], acc, as, ws, j);
+            } else {
+                const float s = mx_scale(ws >> (8 * j) & 255u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        *reinterpret_cast<const h8_t *>(src + 128 * j + 64 * h + 16 * e), mx_decode8(w[j][e], s), acc, 0,
+                        0, 0);
+            }
+        }
+        wave_lds_sync();
+    }
+    // rows 0 .. 7 of C: registers 0 .. 3 of both halves
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (4 * h + j < RT) sums[(wave * RT + 4 * h + j) * 32 + r] = acc[j];
+    __syncthreads();
+    const int m = threadIdx.x >> 3, col = 4 * (threadIdx.x & 7);
+    if (m >= rt.n) return;
+    Epilogue epi = p.epi;
+    if (epi.bias) epi.bias += (size_t)rt.e * p.N;
+    const ColumnEpilogue ce(epi, p.C, 32 * rt.tn + col, p.N);
+    f4_t v[1] = {*reinterpret_cast<const f4_t *>(sums + m * 32 + col)};
+#pragma unroll
+    for (int k = 1; k < kDecodeWaves; ++k) v[0] += *reinterpret_cast<const f4_t *>(sums + (k * RT + m) * 32 + col);
+    ce.put(rt.s0, m, 1, rt.n, v);
+}
+
 }  // namespace
 
 namespace {
-// The most row tiles of `rows` rows that S slots in `groups` groups can make.
-long long most_row_tiles(int S, long long groups, int rows) {
-    if (groups > S) groups = S;
+// ---------------------------------------------------------------------------
+// Which kernel runs. Large tiles move fewer bytes into a CU for each matrix
+// instruction; small ones, and more K groups in a workgroup, keep 256 CUs busy
+// when C is small. Measured on an MI355X (us, M x K x N, the number of tiles
+// in brackets; "64x128/2" is a tile with two K groups):
+//   dense, fp16 activations  128x256     64x256      64x128/2    32x64/4     32x32/8
+//   4096 x 4096 x 4096       115 [512]   121
+//   2048 x 4096 x 4096       69.9 [256]  64.0 [512]  74.9
+//   2048 x 9728 x 2560       125 [160]   115 [320]   116 [640]
+//   512 x 4096 x 4096        52.5        34.7 [128]  22.1 [256]  29.4
+//   128 x 2560 x 9728                    23.6        14.6 [152]  16.9 [608]
+//   128 x 4096 x 4096                                18.9 [64]   11.2 [256]  16.3
+//   32 x 2560 x 9728                                 13.2        8.7 [152]   14.0 [304]
+//   64 x 4096 x 4096                                             10.7 [128]  9.4 [256]
+//   dense, MXFP4 activations
+//   2048 x 9728 x 2560       57.9 [160]  67.5        65.3
+//   512 x 4096 x 4096        23.6 [64]   17.7        14.5 [256]
+// (a stage of the 128 x 256 tile takes more than twice as long with fp16
+// activations, so a second round of such tiles costs more there).
+//   32 experts of 2560 x 4096, fp16: rows of the average expert
+//                            128x256     64x256      32x256      32x128/2    8 rows (decode)
+//   512                      321         311         357         432
+//   32                       69.3        53.4        54.2        57.3
+//   16                       63.6        43.9        41.4        43.9
+//   4                        51.3        34.5        27.9        25.7        41.9
+//   1                        32.5        22.3        19.1        16.3        18.8
+//   the same, MXFP4 activations
+//   512                      151         172         217         300
+//   128                      68.2        68.7        80.8        104
+//   16                       40.0        34.9        36.7        38.6
+//   8                        36.2        32.8        30.9        32.3        61.7
+//   1                        17.5        15.9        15.3        15.9        18.5
+// One token's 8 of 64 experts of 2560 x 2048: 8 rows (decode) 8.2, 2 rows 7.9.
+// ---------------------------------------------------------------------------
+enum Shape { T128x256, T64x256, T64x128, T32x256, T32x128, T32x64, T32x32 };
+constexpr int kTileRows[] = {128, 64, 64, 32, 32, 32, 32}, kTileCols[] = {256, 256, 128, 256, 128, 64, 32};
+constexpr int kEnoughTiles = 144;       // of 256 CUs: from here a larger tile beats more workgroups
+
+// Tiles to expect of S slots in E groups: all their rows in whole tiles, and
+// half a tile more for every group that has rows (with S slots dealt evenly,
+// about S E / (S + E) groups); at least one tile each.
+long long expect_tiles(Shape t, int S, int E, int N) {
+    const int bm = kTileRows[t];
+    long long rows = div_up(S, bm);
+    if (E > 1) {
+        const long long some = (long long)S * E / ((long long)S + E) + 1;
+        rows = S / bm + some / 2 > some ? S / bm + some / 2 : some;
+    }
+    return rows * div_up(N, kTileCols[t]);
+}
+
+Shape dense_shape(bool A4, int M, int N) {
+    auto enough = [&](Shape t, int n) { return expect_tiles(t, M, 1, N) >= n; };
+    if (M > (A4 ? 96 : 384) && enough(T128x256, A4 ? kEnoughTiles : 512)) return T128x256;
+    if (M > 48 && enough(T64x256, 256)) return T64x256;
+    if (M > 32 && enough(T64x128, kEnoughTiles)) return T64x128;
+    return enough(T32x64, kEnoughTiles) ? T32x64 : T32x32;
+}
+
+Shape grouped_shape(bool A4, int S, int E, int N) {
+    auto enough = [&](Shape t) { return expect_tiles(t, S, E, N) >= kEnoughTiles; };
+    const int rows = S / (S < E ? S : E);      // of the average group
+    if (A4 && rows >= 128 && enough(T128x256)) return T128x256;
+    if (rows >= (A4 ? 12 : 24) && enough(T64x256)) return T64x256;
+    if (rows >= 24 && enough(T64x128)) return T64x128;
+    if (rows >= (A4 ? 1 : 6) && enough(T32x256)) return T32x256;
+    if (enough(T32x128)) return T32x128;
+    return enough(T32x64) ? T32x64 : T32x32;
+}
+
+// The most row tiles of `rows` rows that S slots in E groups can make.
+long long most_row_tiles(int S, int E, int rows) {
+    const long long groups = E < S ? E : S;
     return groups + (S - groups) / rows;
 }
 
@@ -553,66 +744,55 @@ hipError_t launch_tile(MxArgs p, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tile shapes, from large to small. Large tiles move fewer bytes into a CU for
-// each matrix instruction; small ones, and more K groups in a workgroup, keep
-// 256 CUs busy when C is small. Which one runs depends on how many tiles it
-// would make, from these measurements (us, MI355X, M x K x N; the tiles of
-// the shape in brackets):
-//   fp16 activations        128x256     64x256      64x128/2    32x64/4     32x32/8
-//   4096 x 4096 x 4096      115 [512]   121
-//   2048 x 4096 x 4096      69.9 [256]  64.0 [512]  74.9
-//   2048 x 9728 x 2560      125 [160]   115 [320]   116 [640]
-//   512 x 4096 x 4096       52.5        34.7 [128]  22.1 [256]  29.4
-//   128 x 2560 x 9728                   23.6        14.6 [152]  16.9 [608]
-//   128 x 4096 x 4096                               18.9 [64]   11.2 [256]  16.3
-//   8 x 2560 x 9728                                 12.8        8.2 [152]   12.5 [304]
-//   64 x 4096 x 4096                                            10.7 [128]  9.4 [256]
-//   MXFP4 activations
-//   2048 x 9728 x 2560      57.9 [160]  67.5        65.3
-//   512 x 4096 x 4096       23.6 [64]   17.7        14.5 [256]
-// (the 128 x 256 tile's stages take twice as long with fp16 activations, so
-// a second round of them costs more there).
-enum Shape { T128x256, T64x256, T64x128, T32x64, T32x32 };
-constexpr int kTileRows[] = {128, 64, 64, 32, 32}, kTileCols[] = {256, 256, 128, 64, 32};
+template <bool A4, int RT, bool ONCE>
+hipError_t launch_decode_rows(MxArgs p, hipStream_t s) {
+    p.tiles_n = div_up(p.N, 32);
+    const long long grid = most_row_tiles(p.S, p.offsets ? p.E : 1, RT) * p.tiles_n;
+    hipLaunchKernelGGL((mx_decode_kernel<A4, RT, ONCE>), dim3((unsigned)((grid + 7) / 8 * 8)),
+                       dim3(64 * kDecodeWaves), 0, s, p);
+    return hipGetLastError();
+}
 
-Shape choose_shape(bool A4, int S, long long groups, int N) {
-    // row tiles to expect: the groups' last tiles are half empty on average
-    auto tiles = [&](Shape t) {
-        const int bm = kTileRows[t];
-        const long long full = groups <= 1 ? (S + bm - 1) / bm : S / bm + (groups < S ? groups : S) / 2;
-        return full * div_up(N, kTileCols[t]);
-    };
-    // rows of the average group: a tile of twice that is mostly padding
-    const long long rows = S / (groups < S ? groups : S);
-    if (rows > (A4 ? 96 : 384) && tiles(T128x256) >= (A4 ? 144 : 512)) return T128x256;
-    if (rows > 48 && tiles(T64x256) >= 256) return T64x256;
-    if (rows > 32 && tiles(T64x128) >= 144) return T64x128;
-    return tiles(T32x64) >= 144 ? T32x64 : T32x32;
+// Up to two rows a group (as far as the host can know): tiles of two rows.
+template <bool A4>
+hipError_t launch_decode(const MxArgs &p, hipStream_t s) {
+    if (!p.offsets)
+        return p.S <= 2 ? launch_decode_rows<A4, 2, true>(p, s) : launch_decode_rows<A4, 8, true>(p, s);
+    return 4LL * p.S <= p.E ? launch_decode_rows<A4, 2, false>(p, s) : launch_decode_rows<A4, 8, false>(p, s);
 }
 
 template <bool A4>
-hipError_t launch_product(const MxArgs &p, hipStream_t s) {
-    switch (choose_shape(A4, p.S, p.offsets ? p.E : 1, p.N)) {
+hipError_t launch_tiles(const MxArgs &p, hipStream_t s) {
+    switch (p.offsets ? grouped_shape(A4, p.S, p.E, p.N) : dense_shape(A4, p.S, p.N)) {
     //                                       RF CF WM WN WK NS BR waves a SIMD
     case T128x256: return launch_tile<Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
     case T64x256:  return launch_tile<Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
     case T64x128:  return launch_tile<Tile<A4, 2, 1, 1, 4, 2, 4, 2, 2>>(p, s);
+    case T32x256:  return launch_tile<Tile<A4, 1, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T32x128:  return launch_tile<Tile<A4, 1, 1, 1, 4, 2, 4, 2, 2>>(p, s);
     case T32x64:   return launch_tile<Tile<A4, 1, 1, 1, 2, 4, 4, 2, 2>>(p, s);
     default:       return launch_tile<Tile<A4, 1, 1, 1, 1, 8, 4, 2, 1>>(p, s);
     }
 }
+
 }  // namespace
 
-hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, void *ws, hipStream_t s) {
+// Few rows a group and too few 32 x 128 tiles to fill the CUs.
+bool mx_grouped_decode(int S, int E, int N) {
+    return S / (S < E ? S : E) <= 2 && expect_tiles(T32x128, S, E, N) < kEnoughTiles;
+}
+
+hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, bool decode, void *ws, hipStream_t s) {
     MxArgs p = args;
-    if (f != QGEMM_MXFP4_A4) return launch_product<false>(p, s);
+    if (f != QGEMM_MXFP4_A4) return decode ? launch_decode<false>(p, s) : launch_tiles<false>(p, s);
+    if (decode) return launch_decode<true>(p, s);
     const MxWorkspace w = mx_workspace(f, p.a_rows, p.K);
     uint8_t *base = static_cast<uint8_t *>(ws);
     const hipError_t e = launch_mx_quantize_act(p.a_rows, p.K, p.A, base, base + w.s_off, s);
     if (e != hipSuccess) return e;
     p.Aq = base;
     p.As = base + w.s_off;
-    return launch_product<true>(p, s);
+    return launch_tiles<true>(p, s);
 }
 
 }  // namespace qg

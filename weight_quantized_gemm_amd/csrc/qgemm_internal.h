@@ -310,7 +310,10 @@ struct MxWorkspace {
 MxWorkspace mx_workspace(qgemm_format f, long long rows, int K);
 // Workgroups of the product's launch, at most (2^31 - 1 are allowed).
 long long mx_grid(int S, int E, int N);
-hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, void *ws, hipStream_t s);
+// decode: the kernel for few rows, which needs no scratch; for the dense product
+// up to the GEMV limit's rows, for a grouped one as mx_grouped_decode says.
+bool mx_grouped_decode(int S, int E, int N);
+hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, bool decode, void *ws, hipStream_t s);
 
 hipError_t launch_mx_quantize(int R, int K, int t, const void *X, size_t ldx, uint8_t *q, uint8_t *scales,
                               hipStream_t s);

@@ -12,6 +12,7 @@ HIP runtime (torch's), which the library then binds to by its soname.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -239,9 +240,14 @@ def _check_run_args(M: int, K: int, N: int, fmt, A, Bq, scales, C, out_type=0, b
                          f"ws_bytes={ws_bytes} claimed")
 
 
+# The current stream's handle without building a Stream object for every call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -261,6 +267,7 @@ def qgemm_canonical_size(K: int, N: int, fmt) -> tuple[int, int]:
     return q.value, p.value
 
 
+@functools.lru_cache(maxsize=4096)
 def qgemm_packed_size(K: int, N: int, fmt) -> tuple[int, int]:
     w, s = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().qgemm_packed_size(K, N, _fmt(fmt), ctypes.byref(w), ctypes.byref(s)),
@@ -430,21 +437,39 @@ def _same_device(**tensors):
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name}: expected a GPU tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
-        dev = t.device
+        d = t.device
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name}: on {d}, the other tensors on {dev}")
     return dev
 
 
 def _exact(t, name: str, dtypes, shape):
     """Checks a tensor's dtype, shape and contiguity."""
-    _need(t, name, dtypes)
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return
+    if t.dtype not in dtypes:
+        want = " or ".join(_TORCH_DTYPE_NAMES.get(d, str(d)) for d in dtypes)
+        raise ValueError(f"{name}: dtype {t.dtype} where {want} is required")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _call(name: str, dev, stream, *args):
+    """Calls an entry point whose last argument is the stream, with `dev` as the
+    current device."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    if stream is None:
+        handle = _raw_stream(dev.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = getattr(load(), name)(*args, handle)
+    if status:
+        raise QGemmError(status, name)
 
 
 def _row_stride(t, name: str) -> int:
@@ -478,9 +503,8 @@ def qgemm_mx_quantize_device(X, q=None, scales=None, stream=None):
         scales = torch.empty((R, K // 32), dtype=torch.uint8, device=dev)
     _exact(q, "q", (torch.uint8,), (R, K // 2))
     _exact(scales, "scales", (torch.uint8,), (R, K // 32))
-    with torch.cuda.device(dev):
-        _check(load().qgemm_mx_quantize_device(R, K, _TYPE_IDS[X.dtype], X.data_ptr(), ld, q.data_ptr(),
-                                               scales.data_ptr(), _stream(stream)), "qgemm_mx_quantize_device")
+    _call("qgemm_mx_quantize_device", dev, stream, R, K, _TYPE_IDS[X.dtype], X.data_ptr(), ld, q.data_ptr(),
+          scales.data_ptr())
     return q, scales
 
 
@@ -500,10 +524,8 @@ def qgemm_mx_dequantize_device(q, scales, dtype="f32", Y=None, stream=None):
     if Y.dtype not in _TYPE_IDS or tuple(Y.shape) != (R, K):
         raise ValueError(f"Y: {Y.dtype} {tuple(Y.shape)}, expected a float tensor of shape {(R, K)}")
     ld = _row_stride(Y, "Y")
-    with torch.cuda.device(dev):
-        _check(load().qgemm_mx_dequantize_device(R, K, q.data_ptr(), scales.data_ptr(), _TYPE_IDS[Y.dtype],
-                                                 Y.data_ptr(), ld, _stream(stream)),
-               "qgemm_mx_dequantize_device")
+    _call("qgemm_mx_dequantize_device", dev, stream, R, K, q.data_ptr(), scales.data_ptr(), _TYPE_IDS[Y.dtype],
+          Y.data_ptr(), ld)
     return Y
 
 
@@ -536,9 +558,7 @@ def qgemm_mx_pack_device(K: int, N: int, q, scales, E: int = 1, Bq=None, Sp=None
         Sp = torch.empty(E * sb, dtype=torch.uint8, device=dev)
     _exact(Bq, "Bq", (torch.uint8,), (E * wb,))
     _exact(Sp, "Sp", (torch.uint8,), (E * sb,))
-    with torch.cuda.device(dev):
-        _check(load().qgemm_mx_pack_device(K, N, E, q.data_ptr(), scales.data_ptr(), Bq.data_ptr(), Sp.data_ptr(),
-                                           _stream(stream)), "qgemm_mx_pack_device")
+    _call("qgemm_mx_pack_device", dev, stream, K, N, E, q.data_ptr(), scales.data_ptr(), Bq.data_ptr(), Sp.data_ptr())
     return Bq, Sp
 
 
@@ -579,11 +599,9 @@ def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace
     _exact(offsets, "offsets", (torch.int32,), (E + 1,))
     _exact(rows, "rows", (torch.int32,), (T * topk,))
     _exact(slots, "slots", (torch.int32,), (T, topk))
-    with torch.cuda.device(dev):
-        _check(load().qgemm_group_plan(T, topk, E, ids.data_ptr(), int(ids.dtype == torch.int64),
-                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
-                                       _scratch(workspace, ws_bytes), ws_bytes, _stream(stream)),
-               "qgemm_group_plan")
+    _call("qgemm_group_plan", dev, stream, T, topk, E, ids.data_ptr(), int(ids.dtype == torch.int64),
+          offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+          _scratch(workspace, ws_bytes), ws_bytes)
     return offsets, rows, slots
 
 
@@ -624,11 +642,9 @@ def qgemm_run_grouped(K: int, N: int, E: int, fmt, A, rows, offsets, Bq, scales,
     epi = Epilogue(_dev_ptr(bias), _dev_ptr(residual),
                    ACTIVATIONS[activation] if isinstance(activation, str) else int(activation),
                    OUT_TYPES[out_type] if isinstance(out_type, str) else int(out_type))
-    with torch.cuda.device(dev):
-        _check(load().qgemm_run_grouped(S, a_rows, K, N, E, f, A.data_ptr(), _dev_ptr(rows), offsets.data_ptr(),
-                                        Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi),
-                                        _scratch(workspace, ws_bytes), ws_bytes, _stream(stream)),
-               "qgemm_run_grouped")
+    _call("qgemm_run_grouped", dev, stream, S, a_rows, K, N, E, f, A.data_ptr(), _dev_ptr(rows), offsets.data_ptr(),
+          Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi),
+          _scratch(workspace, ws_bytes), ws_bytes)
 
 
 def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
@@ -644,10 +660,8 @@ def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
     _exact(slots, "slots", (torch.int32,), (T, topk))
     _exact(weights, "weights", (torch.float32,), (T, topk))
     _exact(C, "C", half, (T, N))
-    with torch.cuda.device(dev):
-        _check(load().qgemm_group_combine(T, topk, N, S, Y.data_ptr(), _TYPE_IDS[Y.dtype], slots.data_ptr(),
-                                          weights.data_ptr(), C.data_ptr(), _TYPE_IDS[C.dtype], _stream(stream)),
-               "qgemm_group_combine")
+    _call("qgemm_group_combine", dev, stream, T, topk, N, S, Y.data_ptr(), _TYPE_IDS[Y.dtype], slots.data_ptr(),
+          weights.data_ptr(), C.data_ptr(), _TYPE_IDS[C.dtype])
 
 
 # ---------------------------------------------------------------------------
