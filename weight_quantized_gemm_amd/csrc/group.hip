@@ -17,9 +17,9 @@ namespace {
 // into first positions.
 //   one workgroup (S up to kPlanOneMax): count, scan, place in one launch;
 //   more: a count launch leaves [workgroup][E + 1] totals in the workspace,
-//   and in the second launch every workgroup sums the columns it needs.
-// Bound by latency, not by bytes (12 bytes a choice): few launches, and no
-// more dependent steps than the wave's run is long.
+//   and in the second launch every workgroup adds up what it needs of them.
+// Bound by latency, not by bytes (12 bytes a choice): few launches, and a
+// wave's run short.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWaves = 16;
 constexpr int kPlanThreads = 64 * kPlanWaves;
@@ -185,18 +185,27 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(int S, int top
     __shared__ int wsum[kPlanWaves];
     int *cnt = lds, *before = lds + kPlanWaves * (E + 1), *all = before + (E + 1);
     const int wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kPlanWaves * (E + 1); i += kPlanThreads) lds[i] = 0;
-    for (int key = threadIdx.x; key <= E; key += kPlanThreads) {
-        int b = 0, a = 0;
-        for (int g = 0; g < (int)gridDim.x; ++g) {
-            const int n = totals[(size_t)g * (E + 1) + key];
-            b += g < (int)blockIdx.x ? n : 0;
-            a += n;
-        }
-        before[key] = b;
-        all[key] = a;
-    }
+    for (int i = threadIdx.x; i < (kPlanWaves + 2) * (E + 1); i += kPlanThreads) lds[i] = 0;
     __syncthreads();
+    // the totals of every workgroup, read in a row and added up per key
+    // (whole numbers: the order does not matter)
+    const int n = (int)gridDim.x * (E + 1), mine = (int)blockIdx.x * (E + 1);
+    const int step = kPlanThreads % (E + 1);
+    int key = threadIdx.x % (E + 1);
+    for (int i = threadIdx.x; i < n; i += 8 * kPlanThreads) {
+        int t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = i + u * kPlanThreads < n ? totals[i + u * kPlanThreads] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (t[u]) {
+                atomicAdd(all + key, t[u]);
+                if (i + u * kPlanThreads < mine) atomicAdd(before + key, t[u]);
+            }
+            key += step;
+            if (key > E) key -= E + 1;
+        }
+    }
     int lo, hi;
     plan_run(S, gridDim.x, blockIdx.x, wave, &lo, &hi);
     plan_count(ids, lo, hi, E, bits, cnt + wave * (E + 1));

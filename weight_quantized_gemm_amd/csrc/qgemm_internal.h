@@ -324,12 +324,18 @@ hipError_t launch_mx_dequantize(int R, int K, const uint8_t *q, const uint8_t *s
 hipError_t launch_mx_pack(int K, int N, int E, const uint8_t *q, const uint8_t *scales, void *wp, void *sp,
                           size_t w_bytes, size_t s_bytes, hipStream_t s);
 
-// Workgroups of the plan for S choices: one while a single workgroup's waves
-// take at most 8 turns of 64 each, else one for every such load, up to 64.
-constexpr int kPlanOneMax = 8192;
+// Workgroups of the plan for S choices: one (a single launch) while its 16
+// waves take a turn or two of 64 choices each, else one for every 1024
+// choices, up to 128 (256 from a million choices on, where the waves' runs
+// cost more than the longer column of totals). Measured at 128 experts (us):
+// 2048 choices 6.7 in one workgroup, 7.7 in two; 4096 choices 10.1 in one, 8.1
+// in four; 2 M choices (64 experts) 52 in 128, 36 in 256.
+constexpr int kPlanOneMax = 2048, kPlanPerGroup = 1024;
 inline int plan_groups(long long S) {
-    const long long g = (S + kPlanOneMax - 1) / kPlanOneMax;
-    return g < 1 ? 1 : g > 64 ? 64 : (int)g;
+    if (S <= kPlanOneMax) return 1;
+    const long long g = (S + kPlanPerGroup - 1) / kPlanPerGroup;
+    const int most = S > (1 << 20) ? 256 : 128;
+    return g > most ? most : (int)g;
 }
 hipError_t launch_group_plan(int S, int topk, int E, const void *ids, bool ids64, int32_t *offsets, int32_t *rows,
                              int32_t *slots, int32_t *totals, hipStream_t s);

@@ -176,10 +176,10 @@ def _dev_ptr(t):
     if t is None:
         return None
     if isinstance(t, int):
-        return ctypes.c_void_p(t)
+        return t
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError("device buffers must be contiguous GPU tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 _TORCH_DTYPE_NAMES = {torch.float32: "float32", torch.float16: "float16", torch.uint8: "uint8",
@@ -197,8 +197,12 @@ def _need(t, name: str, dtypes, numel: int | None = None, nbytes: int | None = N
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch tensor or a device address, got {type(t).__name__}")
-    if t.numel() == 0 and not numel and not nbytes:
+    n = t.numel()
+    if n == 0 and not numel and not nbytes:
         return   # an empty placeholder for an operand the shape never reads
+    if (dtypes is None or t.dtype in dtypes) and (numel is None or n >= numel) and \
+            (nbytes is None or n * t.element_size() >= nbytes):
+        return
     if dtypes is not None and t.dtype not in dtypes:
         want = " or ".join(_TORCH_DTYPE_NAMES.get(d, str(d)) for d in dtypes)
         raise ValueError(f"{name}: dtype {t.dtype} where {want} is required")
@@ -247,8 +251,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return _raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -499,10 +503,12 @@ def qgemm_mx_quantize_device(X, q=None, scales=None, stream=None):
     R, K = X.shape
     if q is None:
         q = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
+    else:
+        _exact(q, "q", (torch.uint8,), (R, K // 2))
     if scales is None:
         scales = torch.empty((R, K // 32), dtype=torch.uint8, device=dev)
-    _exact(q, "q", (torch.uint8,), (R, K // 2))
-    _exact(scales, "scales", (torch.uint8,), (R, K // 32))
+    else:
+        _exact(scales, "scales", (torch.uint8,), (R, K // 32))
     _call("qgemm_mx_quantize_device", dev, stream, R, K, _TYPE_IDS[X.dtype], X.data_ptr(), ld, q.data_ptr(),
           scales.data_ptr())
     return q, scales
@@ -520,10 +526,11 @@ def qgemm_mx_dequantize_device(q, scales, dtype="f32", Y=None, stream=None):
     if Y is None:
         if dtype not in TYPES:
             raise ValueError(f"unknown type {dtype}")
-        Y = torch.empty((R, K), dtype=_TORCH_TYPES[TYPES[dtype]], device=dev)
-    if Y.dtype not in _TYPE_IDS or tuple(Y.shape) != (R, K):
-        raise ValueError(f"Y: {Y.dtype} {tuple(Y.shape)}, expected a float tensor of shape {(R, K)}")
-    ld = _row_stride(Y, "Y")
+        Y, ld = torch.empty((R, K), dtype=_TORCH_TYPES[TYPES[dtype]], device=dev), K
+    else:
+        if Y.dtype not in _TYPE_IDS or Y.shape != (R, K):
+            raise ValueError(f"Y: {Y.dtype} {tuple(Y.shape)}, expected a float tensor of shape {(R, K)}")
+        ld = _row_stride(Y, "Y")
     _call("qgemm_mx_dequantize_device", dev, stream, R, K, q.data_ptr(), scales.data_ptr(), _TYPE_IDS[Y.dtype],
           Y.data_ptr(), ld)
     return Y
@@ -562,6 +569,7 @@ def qgemm_mx_pack_device(K: int, N: int, q, scales, E: int = 1, Bq=None, Sp=None
     return Bq, Sp
 
 
+@functools.lru_cache(maxsize=4096)
 def qgemm_group_plan_size(T: int, topk: int, E: int) -> int:
     b = ctypes.c_size_t()
     _check(load().qgemm_group_plan_size(T, topk, E, ctypes.byref(b)), "qgemm_group_plan_size")
@@ -569,15 +577,25 @@ def qgemm_group_plan_size(T: int, topk: int, E: int) -> int:
 
 
 def _scratch(workspace, ws_bytes: int):
-    """Address of an optional workspace tensor that claims ws_bytes."""
-    if workspace is None:
-        return None
+    """Address of a workspace tensor that claims ws_bytes."""
     have = workspace.numel() * workspace.element_size()
     if have < ws_bytes:
         raise ValueError(f"workspace: {have} bytes, ws_bytes={ws_bytes} claimed")
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     return workspace.data_ptr()
+
+
+def _own_scratch(need: int, workspace, ws_bytes: int, dev, stream):
+    """(address, bytes) of a call's scratch: the caller's, or one from torch's
+    allocator, which hands its memory out and takes it back in the order of the
+    current stream at next to no cost. For a call on another stream that order
+    says nothing, so the library allocates on that stream itself."""
+    if workspace is not None:
+        return _scratch(workspace, ws_bytes), ws_bytes
+    if need == 0 or ws_bytes or stream is not None:
+        return None, ws_bytes
+    return torch.empty(need, dtype=torch.uint8, device=dev).data_ptr(), need
 
 
 def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace=None, ws_bytes: int = 0,
@@ -590,21 +608,26 @@ def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace
         raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T][topk]")
     T, topk = ids.shape
     _exact(ids, "ids", (torch.int32, torch.int64), (T, topk))
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
-    if not 1 <= E <= 1024:
-        raise QGemmError(2, "qgemm_group_plan")
-    offsets = new(E + 1) if offsets is None else offsets
-    rows = new(T * topk) if rows is None else rows
-    slots = new(T, topk) if slots is None else slots
-    _exact(offsets, "offsets", (torch.int32,), (E + 1,))
-    _exact(rows, "rows", (torch.int32,), (T * topk,))
-    _exact(slots, "slots", (torch.int32,), (T, topk))
+    need = qgemm_group_plan_size(T, topk, E)       # raises for a bad size
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _exact(offsets, "offsets", (torch.int32,), (E + 1,))
+    if rows is None:
+        rows = torch.empty(T * topk, dtype=torch.int32, device=dev)
+    else:
+        _exact(rows, "rows", (torch.int32,), (T * topk,))
+    if slots is None:
+        slots = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    else:
+        _exact(slots, "slots", (torch.int32,), (T, topk))
+    workspace, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
     _call("qgemm_group_plan", dev, stream, T, topk, E, ids.data_ptr(), int(ids.dtype == torch.int64),
-          offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
-          _scratch(workspace, ws_bytes), ws_bytes)
+          offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), workspace, ws_bytes)
     return offsets, rows, slots
 
 
+@functools.lru_cache(maxsize=4096)
 def qgemm_grouped_workspace_size(S: int, a_rows: int, K: int, N: int, E: int, fmt) -> int:
     b = ctypes.c_size_t()
     _check(load().qgemm_grouped_workspace_size(S, a_rows, K, N, E, _fmt(fmt), ctypes.byref(b)),
@@ -642,9 +665,10 @@ def qgemm_run_grouped(K: int, N: int, E: int, fmt, A, rows, offsets, Bq, scales,
     epi = Epilogue(_dev_ptr(bias), _dev_ptr(residual),
                    ACTIVATIONS[activation] if isinstance(activation, str) else int(activation),
                    OUT_TYPES[out_type] if isinstance(out_type, str) else int(out_type))
+    need = qgemm_grouped_workspace_size(S, a_rows, K, N, E, f)
+    workspace, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
     _call("qgemm_run_grouped", dev, stream, S, a_rows, K, N, E, f, A.data_ptr(), _dev_ptr(rows), offsets.data_ptr(),
-          Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi),
-          _scratch(workspace, ws_bytes), ws_bytes)
+          Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi), workspace, ws_bytes)
 
 
 def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
