@@ -230,13 +230,22 @@ struct Tile {
     static constexpr int PPR = NS / 2;                    // 16-byte pieces per row
     static constexpr int RPI = 64 / PPR;
     static constexpr int ASC = A4 ? (BM + RPI - 1) / RPI * 1024 : 0;          // bytes of a slot
-    static constexpr int DS = A4 ? (BM / RPI + GW - 1) / GW : 0;
-    static constexpr int SR = A4 ? 2 : BR;                // register slots of the scales
+    static constexpr int DS = A4 ? ((BM + RPI - 1) / RPI + GW - 1) / GW : 0;
+    // register slots of the weights' scales: MXFP4 activations take a stage's
+    // codes step by step, and scales fetched no earlier than its last codes
+    // would be what its first step waits for
+    static constexpr int SR = A4 ? NS : BR;
     // loads issued since the DMA of the next stage when a wave waits for it
     // (the weights' and scales' of that stage, everything of NS - 2 more)
     static constexpr int WAIT = NB + (NS - 2) * (D + NB);
+    // MFMA steps that A is read from LDS ahead of its use: a step of one or two
+    // matrix instructions is much shorter than a read (128 x 4096 x 4096 in
+    // 64 x 128 tiles 21.9 us one step ahead, 20.7 three), a long one with four
+    // or eight gains from two with fp16 activations (512 x 4096 x 4096 in 64 x
+    // 256 tiles 41.4 -> 39.7) but not with MXFP4 ones, which lack the registers
+    static constexpr int PD = RF * CF <= 2 ? 3 : A4 ? 1 : 2;
     // loads issued after the prologue's DMA
-    static constexpr int PRO = A4 ? BR * 4 * CF + 2 * CF : BR * NB;
+    static constexpr int PRO = A4 ? BR * 4 * CF + SR * CF : BR * NB;
     // floats per row of a wave's C block in LDS: rows 4 apart, which one
     // instruction writes, fall into different halves of the banks
     static constexpr int PITCH = 32 * CF + 8;
@@ -330,7 +339,7 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     // soon as its step has run, and the stage's scale words in two slots.
     // fp16 activations: one record and scale byte for the whole stage.
     u4_t bc[BR][CF][T::NREC];
-    unsigned bs[T::SR][CF], as[T::SR][RF];
+    unsigned bs[T::SR][CF], as[2][RF];
     auto load_codes = [&](int j, int rec, int st) {
         const int k = (st0 + min(st, last)) * T::NREC + rec;
 #pragma unroll
@@ -364,7 +373,9 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
     // operands of one MFMA step: s of the stage in LDS slot `slot` and register slot j
-    u4_t a[2][RF];
+    // (A's PD steps ahead)
+    constexpr int PD = T::PD, AR = PD == 1 ? 2 : 4;
+    u4_t a[AR][RF];
     h8_t b[2][CF];
     const unsigned char *const a_lds = mine + (32 * RF * wm + r) * 128;
     auto read_a = [&](u4_t (&dst)[RF], int slot, int s) {
@@ -382,15 +393,15 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
             }
         }
     };
-    auto multiply = [&](int x, int j, int y, int s) {
+    auto multiply = [&](int x, int z, int j, int y, int s) {
 #pragma unroll
         for (int rf = 0; rf < RF; ++rf)
 #pragma unroll
             for (int cf = 0; cf < CF; ++cf) {
                 if constexpr (A4)
-                    acc[rf][cf] = mfma_fp4(a[x][rf], bc[y][cf][s], acc[rf][cf], as[j][rf], bs[j][cf], s);
+                    acc[rf][cf] = mfma_fp4(a[x][rf], bc[y][cf][s], acc[rf][cf], as[j & 1][rf], bs[j][cf], s);
                 else
-                    acc[rf][cf] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, a[x][rf]), b[x][cf],
+                    acc[rf][cf] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, a[x][rf]), b[z][cf],
                                                                          acc[rf][cf], 0, 0, 0);
             }
         if constexpr (A4) {
@@ -427,7 +438,8 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     __builtin_amdgcn_s_waitcnt(vm_wait(T::PRO));
     stage_barrier();
     read_scales(0, 0, 0);
-    read_a(a[0], 0, 0);
+#pragma unroll
+    for (int s = 0; s < PD; ++s) read_a(a[s], 0, s);
     decode_b(b[0], 0, 0);
 
     for (int base = 0; base < nst; base += NS) {
@@ -437,38 +449,40 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
             if (u > 0 && i >= nst) break;          // wave-uniform
             const int j = u % T::SR, y = u % BR;
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                read_a(a[(s + 1) & 1], u, s + 1);
-                decode_b(b[(s + 1) & 1], j, s + 1);
-                multiply(s & 1, j, y, s);
+            for (int s = 0; s < 4; ++s) {
+                if (s == 4 - PD) {
+                    // The reads of this stage are done, and the next ones are
+                    // the next stage's. (No branch here: the optimiser would
+                    // move the matrix instructions above into the block
+                    // behind it, past the loads.)
+                    __builtin_amdgcn_s_waitcnt(stage_wait(T::WAIT));
+                    stage_barrier();
+                    dma(u, i + NS);
+                    // (the other slot's scales, of the turn before, have been read)
+                    if constexpr (A4) {
+                        if (u == 0) dma_scales(base / NS + 1);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    read_scales((u + 1) & 1, base / NS + (u + 1) / NS, (u + 1) % NS);
+                }
+                if (s + PD < 4) read_a(a[(s + PD) % AR], u, s + PD);
+                else read_a(a[(s + PD) % AR], (u + 1) % NS, s + PD - 4);
+                if (s < 3) {
+                    decode_b(b[(s + 1) & 1], j, s + 1);
+                } else {
+                    if constexpr (!A4) {
+                        load_codes(j, 0, i + BR);
+                        load_scales(j, i + BR);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    decode_b(b[0], (u + 1) % T::SR, 0);
+                }
+                multiply(s % AR, s & 1, j, y, s);
                 if constexpr (A4) {
                     load_codes(y, s, i + BR);
+                    if (s == 3) load_scales(j, i + T::SR);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-            // (no branch here: the optimiser would move the matrix
-            // instructions above into the block behind it, past the loads)
-            __builtin_amdgcn_s_waitcnt(stage_wait(T::WAIT));
-            stage_barrier();
-            dma(u, i + NS);
-            // (the other slot's scales, of the turn before, have been read)
-            if constexpr (A4) {
-                if (u == 0) dma_scales(base / NS + 1);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            read_scales((u + 1) % T::SR, base / NS + (u + 1) / NS, (u + 1) % NS);
-            read_a(a[0], (u + 1) % NS, 0);
-            if constexpr (!A4) {
-                load_codes(j, 0, i + BR);
-                load_scales(j, i + BR);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            decode_b(b[0], (u + 1) % T::SR, 0);
-            multiply(1, j, y, 3);
-            if constexpr (A4) {
-                load_codes(y, 3, i + BR);
-                load_scales(j, i + 2);
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -767,7 +781,7 @@ hipError_t launch_tiles(const MxArgs &p, hipStream_t s) {
     //                                       RF CF WM WN WK NS BR waves a SIMD
     case T128x256: return launch_tile<Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
     case T64x256:  return launch_tile<Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
-    case T64x128:  return launch_tile<Tile<A4, 2, 1, 1, 4, 2, 4, 2, 2>>(p, s);
+    case T64x128:  return launch_tile<Tile<A4, 2, 1, 1, 4, A4 ? 2 : 4, 4, 2, A4 ? 2 : 4>>(p, s);
     case T32x256:  return launch_tile<Tile<A4, 1, 2, 1, 4, 1, 4, 2, 2>>(p, s);
     case T32x128:  return launch_tile<Tile<A4, 1, 1, 1, 4, 2, 4, 2, 2>>(p, s);
     case T32x64:   return launch_tile<Tile<A4, 1, 1, 1, 2, 4, 4, 2, 2>>(p, s);
