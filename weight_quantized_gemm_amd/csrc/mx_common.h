@@ -76,52 +76,61 @@ __device__ __forceinline__ RowTile tile_of_group(int e, int lo, int hi, int BM, 
     return RowTile{e, s0, min(BM, hi - s0), tn};
 }
 
+// Inclusive sum over the 64 lanes: within rows of 16 lanes, then row 0's (and
+// 2's) total into the next row, then the lower half's into the upper. (With
+// shuffles through LDS, dependent round trips, finding its tile took a
+// workgroup 2.0 us at 16384 rows over 32 groups; so it takes 1.2.)
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);     // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);     // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);     // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);     // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);     // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);     // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 // The tile of workgroup L of a launch of 8 * per-XCD workgroups, found by the
 // whole wave (every wave of a workgroup does so for itself): each lane counts
 // one group's row tiles, a scan over the lanes adds them up, 64 groups at a
 // time.
 __device__ __forceinline__ RowTile find_tile(const int32_t *__restrict__ offsets, int E, int S, int BM, int tiles_n,
                                              int L) {
-        const int x = L & 7, idx = L >> 3;
+    const int x = L & 7, idx = L >> 3;
     if (!offsets) {
         const int total = (S + BM - 1) / BM * tiles_n, per = (total + 7) >> 3, q = x * per + idx;
         return idx < per && q < total ? tile_of_group(0, 0, S, BM, tiles_n, q) : RowTile{-1, 0, 0, 0};
     }
     const int lane = threadIdx.x & 63;
-    auto bounds = [&](int e, int *lo, int *hi) {
-        *lo = *hi = 0;
-        if (e < E) {
-            *lo = min(max(offsets[e], 0), S);
-            *hi = min(max(offsets[e + 1], *lo), S);
-        }
+    int lo, hi, nt, upto;                 // of group e0 + lane; row tiles of groups e0 .. e0 + lane
+    auto count = [&](int e0) {
+        const int e = min(e0 + lane, E - 1);
+        lo = min(max(offsets[e], 0), S);
+        hi = min(max(offsets[e + 1], lo), S);
+        nt = e0 + lane < E ? (hi - lo + BM - 1) / BM : 0;
+        upto = wave_scan(nt);
     };
-    int lo, hi, all = 0;
+    int all = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
-        bounds(e0 + lane, &lo, &hi);
-        all += (hi - lo + BM - 1) / BM;
+        count(e0);
+        all += __builtin_amdgcn_readlane(upto, 63);
     }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
     const int total = all * tiles_n, per = (total + 7) >> 3, q = x * per + idx;
     if (idx >= per || q >= total) return RowTile{-1, 0, 0, 0};
     int before = 0;                       // row tiles of the groups already passed
     for (int e0 = 0; e0 < E; e0 += 64) {
-        if (E > 64) bounds(e0 + lane, &lo, &hi);
-        const int nt = (hi - lo + BM - 1) / BM;
-        int upto = nt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(upto, d);
-            if (lane >= d) upto += y;
-        }
+        if (E > 64) count(e0);
         const unsigned long long past = __ballot((before + upto) * tiles_n > q);
         if (past) {
             const int src = __ffsll((long long)past) - 1;
-            const int first = uniform(before + __shfl(upto - nt, src));     // row tiles before group src
-            return tile_of_group(uniform(e0 + src), uniform(__shfl(lo, src)), uniform(__shfl(hi, src)), BM, tiles_n,
-                                 q - first * tiles_n);
+            const int first = before + __builtin_amdgcn_readlane(upto - nt, src);     // row tiles before group src
+            const int i = q - first * tiles_n;
+            // (offsets that fall can make the sums above pass 32 bits; one group's tiles do not)
+            if (i < 0 || i >= __builtin_amdgcn_readlane(nt, src) * tiles_n) return RowTile{-1, 0, 0, 0};
+            return tile_of_group(e0 + src, __builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src), BM,
+                                 tiles_n, i);
         }
-        before += __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return RowTile{-1, 0, 0, 0};
 }
