@@ -10,6 +10,8 @@
 // go to v_mfma_scale_f32_32x32x64_f8f6f4 as codes and scale bytes: the 32
 // codes a lane feeds are exactly one scaled block, and a packed 1 KiB record
 // is one operand.
+#include <type_traits>
+
 #include "mx_common.h"
 
 namespace qg {
@@ -102,8 +104,12 @@ __device__ __forceinline__ float silu32(float v) {
 }
 
 // The epilogue of a lane that holds columns n .. n + 3 (n a multiple of 4) of
-// several rows: its bias is loaded once, rows are handled B at a time with
-// every load of a batch requested before the first use.
+// several rows: its bias is loaded once, before any store (a wait for a load
+// waits for the stores issued before it as well), rows are handled B at a
+// time, a batch's loads all requested before the first use. VEC: N is a
+// multiple of 4, so four columns are one vector in every row; otherwise rows
+// of C (and of bias and residual) start anywhere.
+template <bool VEC>
 struct ColumnEpilogue {
     Epilogue epi;
     void *C;
@@ -112,24 +118,32 @@ struct ColumnEpilogue {
 
     __device__ __forceinline__ ColumnEpilogue(const Epilogue &e, void *C_, int n_, int N_)
         : epi(e), C(C_), n(n_), N(N_), bias{0.f, 0.f, 0.f, 0.f} {
-        if (!e.bias) return;
-        if ((N & 3) == 0) {
-            if (n < N) bias = *reinterpret_cast<const f4_t *>(e.bias + n);
-        } else {
+        if (e.bias) {
+            if constexpr (VEC) {
+                bias = *reinterpret_cast<const f4_t *>(e.bias + min(n, N - 4));
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < N) bias[i] = e.bias[n + i];
+                for (int i = 0; i < 4; ++i) bias[i] = e.bias[min(n + i, N - 1)];
+            }
         }
+        asm volatile("" : "+v"(bias));     // here, not in the loops of rows
     }
 
     template <int B>
     __device__ __forceinline__ void activate(f4_t (&v)[B]) const {
         if (epi.act == QGEMM_ACT_NONE) return;
         if (epi.act == QGEMM_ACT_SILU) {
+            if (epi.f16) {
 #pragma unroll
-            for (int i = 0; i < B; ++i)
+                for (int i = 0; i < B; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[i][c] = epi.f16 ? silu16(v[i][c]) : silu32(v[i][c]);
+                    for (int c = 0; c < 4; ++c) v[i][c] = silu16(v[i][c]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = silu32(v[i][c]);
+            }
         } else if (epi.act == QGEMM_ACT_RELU) {
 #pragma unroll
             for (int i = 0; i < B; ++i)
@@ -146,62 +160,55 @@ struct ColumnEpilogue {
         }
     }
 
-    // rows m, m + step, ... (those below `rows`), with values v
+    // rows m, m + step, ... of the `rows` (at least one) from slot0 on, with
+    // values v; those past the last are left out
     template <int B>
     __device__ __forceinline__ void put(size_t slot0, int m, int step, int rows, f4_t (&v)[B]) const {
         if (n >= N) return;
-        if ((N & 3) == 0) {
-            if (epi.residual) {
-                f4_t res[B];
+        size_t at[B];
 #pragma unroll
-                for (int i = 0; i < B; ++i) {
-                    // (a row past the end re-reads the last one, to keep the loads together)
-                    const size_t mn = (slot0 + min(m + i * step, rows - 1)) * N + n;
+        for (int i = 0; i < B; ++i) at[i] = (slot0 + min(m + i * step, rows - 1)) * N + n;
+        if (epi.residual) {
+            // (a row past the last re-reads that one, to keep the loads together)
+            f4_t res[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if constexpr (VEC) {
                     if (epi.f16) {
-                        const h4_t x = *reinterpret_cast<const h4_t *>(static_cast<const _Float16 *>(epi.residual) + mn);
+                        const h4_t x = *reinterpret_cast<const h4_t *>(static_cast<const _Float16 *>(epi.residual) + at[i]);
                         res[i] = f4_t{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
                     } else {
-                        res[i] = *reinterpret_cast<const f4_t *>(static_cast<const float *>(epi.residual) + mn);
+                        res[i] = *reinterpret_cast<const f4_t *>(static_cast<const float *>(epi.residual) + at[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const size_t k = at[i] + min(c, N - 1 - n);
+                        res[i][c] = epi.f16 ? (float)static_cast<const _Float16 *>(epi.residual)[k]
+                                            : static_cast<const float *>(epi.residual)[k];
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < B; ++i) v[i] = (v[i] + bias) + res[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < B; ++i) v[i] = v[i] + bias;
             }
-            activate(v);
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (m + i * step >= rows) return;
-                const size_t mn = (slot0 + m + i * step) * N + n;
+            for (int i = 0; i < B; ++i) v[i] = (v[i] + bias) + res[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < B; ++i) v[i] = v[i] + bias;
+        }
+        activate(v);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (m + i * step >= rows) continue;
+            if constexpr (VEC) {
                 if (epi.f16)
-                    *reinterpret_cast<h4_t *>(static_cast<_Float16 *>(C) + mn) =
+                    *reinterpret_cast<h4_t *>(static_cast<_Float16 *>(C) + at[i]) =
                         h4_t{(_Float16)v[i][0], (_Float16)v[i][1], (_Float16)v[i][2], (_Float16)v[i][3]};
                 else
-                    *reinterpret_cast<f4_t *>(static_cast<float *>(C) + mn) = v[i];
-            }
-        } else {
-            // rows of C (and of bias and residual) start at any column
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const size_t mn = (slot0 + min(m + i * step, rows - 1)) * N + n;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    v[i][c] += bias[c];
-                    if (epi.residual && n + c < N)
-                        v[i][c] += epi.f16 ? (float)static_cast<const _Float16 *>(epi.residual)[mn + c]
-                                           : static_cast<const float *>(epi.residual)[mn + c];
-                }
-            }
-            activate(v);
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (m + i * step >= rows) return;
-                const size_t mn = (slot0 + m + i * step) * N + n;
+                    *reinterpret_cast<f4_t *>(static_cast<float *>(C) + at[i]) = v[i];
+            } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (n + c < N) epi_store(epi, C, mn + c, v[i][c]);
+                    if (n + c < N) epi_store(epi, C, at[i] + c, v[i][c]);
             }
         }
     }
@@ -502,8 +509,51 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     __builtin_amdgcn_s_waitcnt(vm_wait(0));      // no DMA in flight into what follows
     __syncthreads();
     float *const out = reinterpret_cast<float *>(lds);
+    auto store = [&](auto vec) {
+        using CE = ColumnEpilogue<decltype(vec)::value>;
+        if constexpr (WK > 1) {
+            // the K groups' partial tiles, added in the order of K
+            constexpr int TPR = T::BN / 4, STEP = T::THREADS / TPR;      // threads per row, rows per turn
+            static_assert(T::THREADS % TPR == 0, "a thread keeps its columns");
+            const int col = 4 * (threadIdx.x % TPR);
+            const CE ce(epi, p.C, n0 + col, p.N);
+            const float *src = out + (threadIdx.x / TPR) * T::BN + col;
+#pragma unroll 1
+            for (int m = threadIdx.x / TPR; m < rt.n; m += STEP, src += STEP * T::BN) {
+                f4_t v[1] = {*reinterpret_cast<const f4_t *>(src)};
+#pragma unroll
+                for (int g = 1; g < WK; ++g) v[0] += *reinterpret_cast<const f4_t *>(src + g * T::BM * T::BN);
+                ce.put(rt.s0, m, STEP, rt.n, v);
+            }
+        } else {
+            // each wave by itself, 32 rows of its columns at a time
+            constexpr int LPR = 8 * CF, STEP = 64 / LPR;      // lanes per row, rows per turn
+            float *const own = out + wave * 32 * T::PITCH;
+            const int col = 4 * (lane % LPR);
+            const CE ce(epi, p.C, n0 + 32 * CF * wn + col, p.N);
+#pragma unroll
+            for (int rf = 0; rf < RF; ++rf) {
+                const int m0 = 32 * (RF * wm + rf);
+                if (m0 >= rt.n) break;               // wave-uniform
+#pragma unroll
+                for (int cf = 0; cf < CF; ++cf)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        own[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * cf + r] = acc[rf][cf][j];
+                wave_lds_sync();
+#pragma unroll 1
+                for (int m = lane / LPR; m < 32; m += 4 * STEP) {
+                    f4_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = *reinterpret_cast<const f4_t *>(own + (m + i * STEP) * T::PITCH + col);
+                    ce.put(rt.s0, m0 + m, STEP, rt.n, v);
+                }
+                wave_lds_sync();
+            }
+        }
+    };
     if constexpr (WK > 1) {
-        // the K groups' partial tiles, added in the order of K
 #pragma unroll
         for (int rf = 0; rf < RF; ++rf)
 #pragma unroll
@@ -513,45 +563,9 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
                     out[(kg * T::BM + 32 * (RF * wm + rf) + 8 * (j >> 2) + 4 * h + (j & 3)) * T::BN +
                         32 * (CF * wn + cf) + r] = acc[rf][cf][j];
         __syncthreads();
-        constexpr int TPR = T::BN / 4, STEP = T::THREADS / TPR;      // threads per row, rows per turn
-        static_assert(T::THREADS % TPR == 0, "a thread keeps its columns");
-        const int col = 4 * (threadIdx.x % TPR);
-        const ColumnEpilogue ce(epi, p.C, n0 + col, p.N);
-        const float *src = out + (threadIdx.x / TPR) * T::BN + col;
-#pragma unroll 1
-        for (int m = threadIdx.x / TPR; m < rt.n; m += STEP, src += STEP * T::BN) {
-            f4_t v[1] = {*reinterpret_cast<const f4_t *>(src)};
-#pragma unroll
-            for (int g = 1; g < WK; ++g) v[0] += *reinterpret_cast<const f4_t *>(src + g * T::BM * T::BN);
-            ce.put(rt.s0, m, STEP, rt.n, v);
-        }
-    } else {
-        // each wave by itself, 32 rows of its columns at a time
-        float *const own = out + wave * 32 * T::PITCH;
-        constexpr int LPR = 8 * CF, STEP = 64 / LPR;      // lanes per row, rows per turn
-        const int col = 4 * (lane % LPR);
-        const ColumnEpilogue ce(epi, p.C, n0 + 32 * CF * wn + col, p.N);
-#pragma unroll
-        for (int rf = 0; rf < RF; ++rf) {
-            const int m0 = 32 * (RF * wm + rf);
-            if (m0 >= rt.n) break;               // wave-uniform
-#pragma unroll
-            for (int cf = 0; cf < CF; ++cf)
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    own[(8 * (j >> 2) + 4 * h + (j & 3)) * T::PITCH + 32 * cf + r] = acc[rf][cf][j];
-            wave_lds_sync();
-#pragma unroll 1
-            for (int m = lane / LPR; m < 32; m += 4 * STEP) {
-                f4_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = *reinterpret_cast<const f4_t *>(own + (m + i * STEP) * T::PITCH + col);
-                if (m0 + m < rt.n) ce.put(rt.s0, m0 + m, STEP, rt.n, v);
-            }
-            wave_lds_sync();
-        }
     }
+    if ((p.N & 3) == 0) store(std::true_type{});
+    else store(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -664,11 +678,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void mx_decode_kernel(MxArgs p) 
     if (m >= rt.n) return;
     Epilogue epi = p.epi;
     if (epi.bias) epi.bias += (size_t)rt.e * p.N;
-    const ColumnEpilogue ce(epi, p.C, 32 * rt.tn + col, p.N);
     f4_t v[1] = {*reinterpret_cast<const f4_t *>(sums + m * 32 + col)};
 #pragma unroll
     for (int k = 1; k < kDecodeWaves; ++k) v[0] += *reinterpret_cast<const f4_t *>(sums + (k * RT + m) * 32 + col);
-    ce.put(rt.s0, m, 1, rt.n, v);
+    if ((p.N & 3) == 0) ColumnEpilogue<true>(epi, p.C, 32 * rt.tn + col, p.N).put(rt.s0, m, 1, rt.n, v);
+    else ColumnEpilogue<false>(epi, p.C, 32 * rt.tn + col, p.N).put(rt.s0, m, 1, rt.n, v);
 }
 
 }  // namespace
