@@ -369,3 +369,15 @@ def test_two_streams_at_once():
                 _forward(up, down, x, ids, wt, E, out)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+def test_combine_more_tokens_than_one_launch_axis():
+    """More workgroups than one axis of a launch may have threads for (2^32)."""
+    T, S = (1 << 24) + 70001, 1000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    Y = torch.randn((S, 1), device="cuda", generator=g)
+    slots = torch.randint(0, S, (T, 1), device="cuda", generator=g, dtype=torch.int32)
+    w = torch.rand((T, 1), device="cuda", generator=g)
+    C = torch.full((T, 1), float("nan"), device="cuda")
+    Q.qgemm_group_combine(Y, slots, w, C)
+    assert torch.equal(C, w * Y[slots[:, 0].long()])     # one product, rounded once

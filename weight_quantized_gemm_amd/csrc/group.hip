@@ -238,18 +238,24 @@ hipError_t plan(int S, int topk, int E, const I *ids, int32_t *offsets, int32_t 
 // Combine: C[t][n] = sum_j weights[t][j] * Y[slots[t][j]][n], j ascending,
 // fp32 fused multiply-adds, one rounding. A thread owns VEC neighbouring
 // columns of one token: every row of Y is read once in whole vectors, C is
-// written once, and no atomics are needed. Bound by memory.
+// written once, and no atomics are needed. Bound by memory: 4099 tokens of 4
+// fp16 rows of 4096 columns (168 MB) 27 us, as fast as a large copy; 16 tokens
+// of 8 rows 3.6 us, of which most is the launch.
+// Block x covers one of `cols` column strips of one of `per` tokens, block y
+// the next `per`: the threads of a launch along x must stay below 2^32.
 // ---------------------------------------------------------------------------
+constexpr unsigned kCombineX = 1u << 22;      // workgroups of 256 threads along x, at most
+
 template <class TY, class TC, int VEC>
 __global__ __launch_bounds__(256) void combine_kernel(int T, int topk, int N, int S, const TY *__restrict__ Y,
                                                       const int32_t *__restrict__ slots,
                                                       const float *__restrict__ weights, TC *__restrict__ C,
-                                                      int cols) {
+                                                      unsigned cols, unsigned per) {
     typedef TY yv __attribute__((ext_vector_type(VEC)));
     typedef TC cv __attribute__((ext_vector_type(VEC)));
-    const size_t t = blockIdx.x / cols;
+    const size_t t = (size_t)blockIdx.y * per + blockIdx.x / cols;
     const int n = ((int)(blockIdx.x % cols) * 256 + (int)threadIdx.x) * VEC;
-    if (n >= N) return;
+    if (n >= N || t >= (size_t)T) return;
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
@@ -269,20 +275,22 @@ __global__ __launch_bounds__(256) void combine_kernel(int T, int topk, int N, in
     *reinterpret_cast<cv *>(C + t * N + n) = o;
 }
 
+template <class TY, class TC, int VEC>
+hipError_t combine_vec(int T, int topk, int N, int S, const void *Y, const int32_t *slots, const float *weights,
+                       void *C, hipStream_t s) {
+    const unsigned cols = (unsigned)div_up(N, 256 * VEC), most = kCombineX / cols;
+    const unsigned per = (unsigned)T < most ? (unsigned)T : most;
+    hipLaunchKernelGGL((combine_kernel<TY, TC, VEC>), dim3(per * cols, ((unsigned)T + per - 1) / per), dim3(256), 0, s,
+                       T, topk, N, S, static_cast<const TY *>(Y), slots, weights, static_cast<TC *>(C), cols, per);
+    return hipGetLastError();
+}
+
+// Whole vectors only where every row of Y and C starts on a vector.
 template <class TY, class TC>
 hipError_t combine(int T, int topk, int N, int S, const void *Y, const int32_t *slots, const float *weights,
                    void *C, hipStream_t s) {
-    // whole vectors only where every row of Y and C starts on a vector
-    if (N % 8 == 0) {
-        const int cols = div_up(N, 256 * 8);
-        hipLaunchKernelGGL((combine_kernel<TY, TC, 8>), dim3((unsigned)T * cols), dim3(256), 0, s, T, topk, N, S,
-                           static_cast<const TY *>(Y), slots, weights, static_cast<TC *>(C), cols);
-    } else {
-        const int cols = div_up(N, 256);
-        hipLaunchKernelGGL((combine_kernel<TY, TC, 1>), dim3((unsigned)T * cols), dim3(256), 0, s, T, topk, N, S,
-                           static_cast<const TY *>(Y), slots, weights, static_cast<TC *>(C), cols);
-    }
-    return hipGetLastError();
+    return N % 8 == 0 ? combine_vec<TY, TC, 8>(T, topk, N, S, Y, slots, weights, C, s)
+                      : combine_vec<TY, TC, 1>(T, topk, N, S, Y, slots, weights, C, s);
 }
 
 }  // namespace
