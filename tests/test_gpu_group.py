@@ -381,3 +381,31 @@ def test_combine_more_tokens_than_one_launch_axis():
     C = torch.full((T, 1), float("nan"), device="cuda")
     Q.qgemm_group_combine(Y, slots, w, C)
     assert torch.equal(C, w * Y[slots[:, 0].long()])     # one product, rounded once
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_belong_to_the_stream_of_the_call(handle):
+    """Results allocated for a call on another stream do not take memory that
+    work of the current stream may still use."""
+    ids = torch.randint(0, 8, (70000, 3), device="cuda", dtype=torch.int32)
+    x = torch.randn((1024, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    given = side.cuda_stream if handle else side
+    sizes = {"rows": 70000 * 3 * 4, "q": 1024 * 2048, "y": 1024 * 4096 * 4}
+    freed = {}
+    for name, n in sizes.items():
+        t = torch.empty(n, dtype=torch.uint8, device="cuda")
+        freed[name] = t.data_ptr()
+        del t
+    want = [t.clone() for t in Q.qgemm_group_plan(ids, 8)]
+    torch.cuda.synchronize()
+    offsets, rows, slots = Q.qgemm_group_plan(ids, 8, stream=given)
+    q, s = Q.qgemm_mx_quantize_device(x, stream=given)
+    y = Q.qgemm_mx_dequantize_device(q, s, stream=given)
+    torch.cuda.synchronize()
+    again = {n: torch.empty(b, dtype=torch.uint8, device="cuda").data_ptr() for n, b in sizes.items()}
+    for t in (rows, slots, q, y):
+        assert t.data_ptr() not in freed.values() and t.data_ptr() not in again.values()
+    assert all(torch.equal(a, b) for a, b in zip(want, (offsets, rows, slots)))
+    assert np.array_equal(y.cpu().numpy(), X.decode(*X.encode(x.cpu().numpy())).astype(np.float32))

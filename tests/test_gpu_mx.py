@@ -276,3 +276,34 @@ def test_untouched_past_the_end():
             buf = torch.full((M * N + 512,), 3.0, device="cuda")
             Q.qgemm_run(M, K, N, fmt, dev(A), w.Bq, w.scales, buf[:M * N].view(M, N))
             assert (buf[M * N:] == 3.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_weights_outside_fp16(M):
+    """The product with fp16 activations takes the weights in fp16: rounded
+    once where they are small, infinite where they are too large."""
+    K, N = 128, 64
+    rng = np.random.default_rng(M)
+    W = rng.standard_normal((N, K)).astype(np.float32)
+    W[:32] *= (2.0 ** -rng.integers(14, 30, (32, 1))).astype(np.float32)     # down to zeros
+    W[32:] *= (2.0 ** rng.integers(10, 14, (32, 1))).astype(np.float32)
+    W[50] = 2.0 ** 20
+    q, s = X.encode(W)
+    with np.errstate(over="ignore"):
+        w16 = X.decode(q, s).astype(np.float16).astype(np.float64)
+    assert np.isinf(w16[50]).all() and (w16[:32] == 0).any()
+    A = np.abs(rng.standard_normal((M, K))).astype(np.float16) + np.float16(0.5)
+    C = Q.PackedWeight("mxfp4", K, N, q, s)(dev(A)).cpu().numpy()
+    fine = np.isfinite(w16).all(1)
+    assert np.isposinf(C[:, ~fine][:, :1]).all() and np.isposinf(C[:, 50]).all()
+    a = A.astype(np.float64)
+    X.check_product(C[:, fine], a @ w16[fine].T, np.abs(a) @ np.abs(w16[fine]).T, K)
+
+
+def test_pack_refuses_strided_codes():
+    q = torch.zeros((32, 64), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((32, 4), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        Q.qgemm_mx_pack_device(64, 32, q[:, :32], s[:, :2].contiguous())
+    with pytest.raises(ValueError):
+        Q.qgemm_mx_pack_device(64, 32, q[:, :32].contiguous(), s[:, :2])

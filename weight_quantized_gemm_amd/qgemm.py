@@ -476,6 +476,19 @@ def _call(name: str, dev, stream, *args):
         raise QGemmError(status, name)
 
 
+def _empty(shape, dtype, dev, stream):
+    """A new tensor for a call on `stream` (None: the current one). Its memory
+    belongs to that stream: memory of the current one may still be in use by
+    work queued there, which a call on another stream does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _row_stride(t, name: str) -> int:
     """Row stride of a [R][K] tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
@@ -502,11 +515,11 @@ def qgemm_mx_quantize_device(X, q=None, scales=None, stream=None):
     ld = _row_stride(X, "X")
     R, K = X.shape
     if q is None:
-        q = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
+        q = _empty((R, K // 2), torch.uint8, dev, stream)
     else:
         _exact(q, "q", (torch.uint8,), (R, K // 2))
     if scales is None:
-        scales = torch.empty((R, K // 32), dtype=torch.uint8, device=dev)
+        scales = _empty((R, K // 32), torch.uint8, dev, stream)
     else:
         _exact(scales, "scales", (torch.uint8,), (R, K // 32))
     _call("qgemm_mx_quantize_device", dev, stream, R, K, _TYPE_IDS[X.dtype], X.data_ptr(), ld, q.data_ptr(),
@@ -526,7 +539,7 @@ def qgemm_mx_dequantize_device(q, scales, dtype="f32", Y=None, stream=None):
     if Y is None:
         if dtype not in TYPES:
             raise ValueError(f"unknown type {dtype}")
-        Y, ld = torch.empty((R, K), dtype=_TORCH_TYPES[TYPES[dtype]], device=dev), K
+        Y, ld = _empty((R, K), _TORCH_TYPES[TYPES[dtype]], dev, stream), K
     else:
         if Y.dtype not in _TYPE_IDS or Y.shape != (R, K):
             raise ValueError(f"Y: {Y.dtype} {tuple(Y.shape)}, expected a float tensor of shape {(R, K)}")
@@ -556,13 +569,14 @@ def qgemm_mx_pack_device(K: int, N: int, q, scales, E: int = 1, Bq=None, Sp=None
     weights, uint8 device tensors, one weight after the other."""
     dev = _same_device(q=q, scales=scales, Bq=Bq, Sp=Sp)
     wb, sb = qgemm_packed_size(K, N, QGEMM_MXFP4)
-    _exact(q.reshape(-1), "q", (torch.uint8,), (E * N * (K // 2),))
-    _exact(scales.reshape(-1), "scales", (torch.uint8,), (E * N * (K // 32),))
-    q, scales = q.contiguous(), scales.contiguous()
+    for t, name, size in ((q, "q", E * N * (K // 2)), (scales, "scales", E * N * (K // 32))):
+        if not t.is_contiguous():          # (a copy would be made on the current stream)
+            raise ValueError(f"{name}: must be contiguous")
+        _exact(t.view(-1), name, (torch.uint8,), (size,))
     if Bq is None:
-        Bq = torch.empty(E * wb, dtype=torch.uint8, device=dev)
+        Bq = _empty(E * wb, torch.uint8, dev, stream)
     if Sp is None:
-        Sp = torch.empty(E * sb, dtype=torch.uint8, device=dev)
+        Sp = _empty(E * sb, torch.uint8, dev, stream)
     _exact(Bq, "Bq", (torch.uint8,), (E * wb,))
     _exact(Sp, "Sp", (torch.uint8,), (E * sb,))
     _call("qgemm_mx_pack_device", dev, stream, K, N, E, q.data_ptr(), scales.data_ptr(), Bq.data_ptr(), Sp.data_ptr())
@@ -610,15 +624,15 @@ def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace
     _exact(ids, "ids", (torch.int32, torch.int64), (T, topk))
     need = qgemm_group_plan_size(T, topk, E)       # raises for a bad size
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        offsets = _empty(E + 1, torch.int32, dev, stream)
     else:
         _exact(offsets, "offsets", (torch.int32,), (E + 1,))
     if rows is None:
-        rows = torch.empty(T * topk, dtype=torch.int32, device=dev)
+        rows = _empty(T * topk, torch.int32, dev, stream)
     else:
         _exact(rows, "rows", (torch.int32,), (T * topk,))
     if slots is None:
-        slots = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        slots = _empty((T, topk), torch.int32, dev, stream)
     else:
         _exact(slots, "slots", (torch.int32,), (T, topk))
     workspace, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
