@@ -35,10 +35,14 @@
  *
  *   QGEMM_MXFP4     microscaled 4-bit floats (OCP Microscaling Formats v1.0,
  *                   MXFP4): E2M1 codes and one E8M0 scale (a power of two) per
- *                   32 K-elements; fp16 activations. K % 64 == 0.
+ *                   32 K-elements; fp16 activations. K % 64 == 0. The product
+ *                   takes the weights in fp16: exact for scales 2^-23 ..
+ *                   2^13, rounded once below (to subnormals and zero), and
+ *                   infinite above 65504.
  *   QGEMM_MXFP4_A4  MXFP4 weights as above, and every row of A quantised to
  *                   MXFP4 on the fly: both operands enter the matrix cores as
- *                   4-bit codes with their scales, fp32 accumulation.
+ *                   4-bit codes with their scales, fp32 accumulation, for
+ *                   every scale.
  *
  * Format ids 0-3 equal the page's mode numbers. For every format but F32, A
  * is fp16; C is fp32 (or fp16 through qgemm_run_ex).

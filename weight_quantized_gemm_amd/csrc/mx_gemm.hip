@@ -692,34 +692,36 @@ namespace {
 // Which kernel runs. Large tiles move fewer bytes into a CU for each matrix
 // instruction; small ones, and more K groups in a workgroup, keep 256 CUs busy
 // when C is small. Measured on an MI355X (us, M x K x N, the number of tiles
-// in brackets; "64x128/2" is a tile with two K groups):
-//   dense, fp16 activations  128x256     64x256      64x128/2    32x64/4     32x32/8
-//   4096 x 4096 x 4096       115 [512]   121
-//   2048 x 4096 x 4096       69.9 [256]  64.0 [512]  74.9
-//   2048 x 9728 x 2560       125 [160]   115 [320]   116 [640]
-//   512 x 4096 x 4096        52.5        34.7 [128]  22.1 [256]  29.4
-//   128 x 2560 x 9728                    23.6        14.6 [152]  16.9 [608]
-//   128 x 4096 x 4096                                18.9 [64]   11.2 [256]  16.3
-//   32 x 2560 x 9728                                 13.2        8.7 [152]   14.0 [304]
-//   64 x 4096 x 4096                                             10.7 [128]  9.4 [256]
-//   dense, MXFP4 activations
-//   2048 x 9728 x 2560       57.9 [160]  67.5        65.3
-//   512 x 4096 x 4096        23.6 [64]   17.7        14.5 [256]
+// in brackets; "64x128/4" is a tile with four K groups):
+//   dense, fp16 activations  128x256     64x256      64x128/4    32x64/4     32x32/8
+//   4096 x 4096 x 4096       110 [512]   122         173
+//   2048 x 4096 x 4096       64.1 [256]  65.7 [512]  90.1
+//   2048 x 9728 x 2560       118 [160]   115 [320]   129
+//   512 x 4096 x 4096        53.5        40.0 [128]  25.4 [256]  35.8
+//   128 x 2560 x 9728                    28.2        18.1 [152]  21.7 [608]  36.0
+//   128 x 4096 x 4096                    37.2        19.6 [64]   12.3 [256]  18.8
+//   32 x 2560 x 9728                                 14.5        10.8 [152]  16.2 [304]
+//   64 x 4096 x 4096                                 18.8        11.8 [128]  10.2 [256]
+//   dense, MXFP4 activations                         64x128/2
+//   2048 x 9728 x 2560       59.2 [160]  70.5        69.2
+//   512 x 4096 x 4096        28.2 [64]   22.0        17.3 [256]
 // (a stage of the 128 x 256 tile takes more than twice as long with fp16
-// activations, so a second round of such tiles costs more there).
+// activations, so a second round of such tiles costs more there. Not kept:
+// 96 x 256 tiles, 2048 x 4096 x 11008 with MXFP4 activations 74.3 as with 128
+// x 256, 16384 rows over 32 experts 144 against 132.)
 //   32 experts of 2560 x 4096, fp16: rows of the average expert
 //                            128x256     64x256      32x256      32x128/2    8 rows (decode)
-//   512                      321         311         357         432
-//   32                       69.3        53.4        54.2        57.3
-//   16                       63.6        43.9        41.4        43.9
-//   4                        51.3        34.5        27.9        25.7        41.9
-//   1                        32.5        22.3        19.1        16.3        18.8
+//   512                      316         314         362         430
+//   32                       75.3        54.3        53.3        55.9
+//   16                       63.8        45.1        41.6        41.9
+//   4                        52.5        34.8        28.2        24.8        41.9
+//   1                        35.2        25.0        22.6        16.7        18.8
 //   the same, MXFP4 activations
-//   512                      151         172         217         300
-//   128                      68.2        68.7        80.8        104
-//   16                       40.0        34.9        36.7        38.6
-//   8                        36.2        32.8        30.9        32.3        61.7
-//   1                        17.5        15.9        15.3        15.9        18.5
+//   512                      152         174         221         289
+//   128                      68.1        67.3        81.2        101
+//   16                       41.5        35.9        36.9        37.4
+//   8                        38.4        34.8        31.2        31.9        61.7
+//   1                        18.6        16.3        15.8        16.0        18.5
 // One token's 8 of 64 experts of 2560 x 2048: 8 rows (decode) 8.2, 2 rows 7.9.
 // ---------------------------------------------------------------------------
 enum Shape { T128x256, T64x256, T64x128, T32x256, T32x128, T32x64, T32x32 };

@@ -95,8 +95,8 @@ constexpr int kMaxBlock = 1 << 24;
 inline bool is_int4_blocked(int f) {
     return f > QGEMM_INT4_BLOCK_BASE && f <= QGEMM_INT4_BLOCK_BASE + kMaxBlock;
 }
-// Int8 with a block size in the format id (QGEMM_INT8_BLOCK(b)).
 inline bool is_mx(int f) { return f == QGEMM_MXFP4 || f == QGEMM_MXFP4_A4; }
+// Int8 with a block size in the format id (QGEMM_INT8_BLOCK(b)).
 inline bool is_int8_blocked(int f) {
     return f > QGEMM_INT8_BLOCK_BASE && f <= QGEMM_INT8_BLOCK_BASE + kMaxBlock;
 }
@@ -289,7 +289,7 @@ __host__ __device__ inline size_t mx_weight_scale(size_t n, unsigned b, unsigned
 }
 
 // One product, dense or grouped: slots [0, S) of C, each reading row rows[s]
-// of A (s itself without `rows`), in E groups (see find_row_tile).
+// of A (s itself without `rows`), in E groups (see find_tile).
 struct MxArgs {
     int S, a_rows, K, N, E;
     const void *A;                    // fp16 [a_rows][K]
