@@ -449,49 +449,58 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     for (int s = 0; s < PD; ++s) read_a(a[s], 0, s);
     decode_b(b[0], 0, 0);
 
-    for (int base = 0; base < nst; base += NS) {
+    auto stage = [&](int base, int u) {
+        const int i = base + u;
+        const int j = u % T::SR, y = u % BR;
 #pragma unroll
-        for (int u = 0; u < NS; ++u) {
-            const int i = base + u;
-            if (u > 0 && i >= nst) break;          // wave-uniform
-            const int j = u % T::SR, y = u % BR;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s == 4 - PD) {
-                    // The reads of this stage are done, and the next ones are
-                    // the next stage's. (No branch here: the optimiser would
-                    // move the matrix instructions above into the block
-                    // behind it, past the loads.)
-                    __builtin_amdgcn_s_waitcnt(stage_wait(T::WAIT));
-                    stage_barrier();
-                    dma(u, i + NS);
-                    // (the other slot's scales, of the turn before, have been read)
-                    if constexpr (A4) {
-                        if (u == 0) dma_scales(base / NS + 1);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                    read_scales((u + 1) & 1, base / NS + (u + 1) / NS, (u + 1) % NS);
-                }
-                if (s + PD < 4) read_a(a[(s + PD) % AR], u, s + PD);
-                else read_a(a[(s + PD) % AR], (u + 1) % NS, s + PD - 4);
-                if (s < 3) {
-                    decode_b(b[(s + 1) & 1], j, s + 1);
-                } else {
-                    if constexpr (!A4) {
-                        load_codes(j, 0, i + BR);
-                        load_scales(j, i + BR);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    decode_b(b[0], (u + 1) % T::SR, 0);
-                }
-                multiply(s % AR, s & 1, j, y, s);
+        for (int s = 0; s < 4; ++s) {
+            if (s == 4 - PD) {
+                // The reads of this stage are done, and the next ones are
+                // the next stage's. (No branch here: the optimiser would
+                // move the matrix instructions above into the block
+                // behind it, past the loads.)
+                __builtin_amdgcn_s_waitcnt(stage_wait(T::WAIT));
+                stage_barrier();
+                dma(u, i + NS);
+                // (the other slot's scales, of the turn before, have been read)
                 if constexpr (A4) {
-                    load_codes(y, s, i + BR);
-                    if (s == 3) load_scales(j, i + T::SR);
+                    if (u == 0) dma_scales(base / NS + 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                read_scales((u + 1) & 1, base / NS + (u + 1) / NS, (u + 1) % NS);
+            }
+            if (s + PD < 4) read_a(a[(s + PD) % AR], u, s + PD);
+            else read_a(a[(s + PD) % AR], (u + 1) % NS, s + PD - 4);
+            if (s < 3) {
+                decode_b(b[(s + 1) & 1], j, s + 1);
+            } else {
+                if constexpr (!A4) {
+                    load_codes(j, 0, i + BR);
+                    load_scales(j, i + BR);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                decode_b(b[0], (u + 1) % T::SR, 0);
+            }
+            multiply(s % AR, s & 1, j, y, s);
+            if constexpr (A4) {
+                load_codes(y, s, i + BR);
+                if (s == 3) load_scales(j, i + T::SR);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+    };
+    // Whole turns, then the stages that are left: with a way out of the middle
+    // of a turn the compiler takes it for a way back to the top as well, and
+    // waits there, every turn, for all loads in flight.
+    int base = 0;
+    for (; base + NS <= nst; base += NS) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) stage(base, u);
+    }
+#pragma unroll
+    for (int u = 0; u < NS - 1; ++u) {
+        if (base + u >= nst) break;            // wave-uniform
+        stage(base, u);
     }
 
     // every wave of the workgroup meets as many barriers
