@@ -96,3 +96,29 @@ def test_replay_catches_a_short_wait():
     entry = dma * 4 + ["s_waitcnt vmcnt(0)", "s_barrier"]
     assert replay(entry, stage(2 + 2 * 6) * 4, 2)[0] == []
     assert replay(entry, stage(2 + 3 * 6) * 4, 2)[0]
+
+
+@pytest.mark.skipif(not (shutil.which(HIPCC) or os.path.exists(HIPCC)), reason="hipcc not found")
+def test_the_stages_behind_the_loop_wait_as_well(tmp_path):
+    """The NS - 1 stages that may follow the whole turns, with the queue that a
+    turn leaves and with the one that the entry leaves (K of fewer stages)."""
+    asm = _asm(str(tmp_path), "mx_gemm.hip")
+    lines = asm.splitlines()
+    seen, problems = 0, []
+    for name, entry, body in main_loops(asm, "mx_tile_kernel"):
+        ns = int(re.search(r"TileILb([01])E" + r"Li(\d+)E" * 8, name).group(7))
+        start = next(i for i, ln in enumerate(lines) if ln.startswith(name + ":")) + len(entry) + len(body)
+        tail, barriers = [], 0
+        for ln in lines[start:]:
+            tail.append(ln)
+            barriers += ln.strip().startswith("s_barrier")
+            if barriers == ns - 1:
+                break
+        assert sum("v_mfma" in ln for ln in tail) > 0 and sum(" lds" in ln for ln in tail) > 0, name
+        for before in (entry, entry + body + body):
+            bad, met = replay(before, tail, ns - 2)
+            assert met == 2 * (ns - 1), name
+            problems += [f"{name[:90]}: {b}" for b in bad]
+        seen += 1
+    assert seen >= 10
+    assert not problems, "\n".join(problems[:20])
