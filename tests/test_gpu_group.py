@@ -409,3 +409,37 @@ def test_outputs_belong_to_the_stream_of_the_call(handle):
         assert t.data_ptr() not in freed.values() and t.data_ptr() not in again.values()
     assert all(torch.equal(a, b) for a, b in zip(want, (offsets, rows, slots)))
     assert np.array_equal(y.cpu().numpy(), X.decode(*X.encode(x.cpu().numpy())).astype(np.float32))
+
+
+@pytest.mark.parametrize("K", [64, 192, 448, 832, 1088, 1344])
+@pytest.mark.parametrize("mean", [1, 4, 8, 40, 130, 300])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_every_tile_of_the_grouped_product(fmt, mean, K):
+    """Groups of every size class (empty ones and parts of tiles among them)
+    over enough columns for the large tiles, rows gathered, K of every number
+    of stages left over; references on the GPU in 64 bits, bounds as in
+    check_product."""
+    E, N = 12, 4100
+    rng = np.random.default_rng(mean + K)
+    sizes = rng.integers(0, 2 * mean + 1, E)
+    sizes[0], sizes[E - 1] = 2 * mean, 0
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    n = int(offsets[-1])
+    T, S = max(3, n // 3), n + 7
+    g = torch.Generator(device="cuda").manual_seed(mean + K)
+    A = torch.randn((T, K), device="cuda", generator=g).half()
+    W = torch.randn((E * N, K), device="cuda", generator=g)
+    rows = torch.randint(0, T, (S,), device="cuda", generator=g, dtype=torch.int32)
+    q, s = Q.qgemm_mx_quantize_device(W)
+    w = Q.qgemm_mx_dequantize_device(q, s).view(E, N, K)
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, q, s, E=E)
+    C = torch.full((S, N), 9.0, device="cuda")
+    Q.qgemm_run_grouped(K, N, E, fmt, A, rows, dev(offsets), Bq, Sp, C)
+    a = Q.qgemm_mx_dequantize_device(*Q.qgemm_mx_quantize_device(A)).double() if fmt == "mxfp4a4" else A.double()
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        x, we = a[rows[lo:hi].long()], w[e].double()
+        ref, mass = x @ we.t(), x.abs() @ we.abs().t()
+        err = (C[lo:hi].double() - ref).abs()
+        assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 1e-37).all()), e
+    assert bool((C[n:] == 9.0).all())

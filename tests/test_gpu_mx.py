@@ -307,3 +307,30 @@ def test_pack_refuses_strided_codes():
         Q.qgemm_mx_pack_device(64, 32, q[:, :32], s[:, :2].contiguous())
     with pytest.raises(ValueError):
         Q.qgemm_mx_pack_device(64, 32, q[:, :32].contiguous(), s[:, :2])
+
+
+# (M, N) of every tile shape the dense dispatch knows, with a ragged last tile
+# of rows and of columns
+TILES = [(1000, 16300), (250, 16300), (40, 18500), (30, 9300), (20, 200)]
+
+
+@pytest.mark.parametrize("K", [64, 192, 320, 448, 576, 832, 1088, 1344, 2112])
+@pytest.mark.parametrize("M,N", TILES)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_every_tile_with_stages_left_over(fmt, M, N, K):
+    """K of whole turns of the main loop and of every number of stages more,
+    fewer stages than K groups among them; references on the GPU in 64 bits,
+    bounds as in check_product."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    A = torch.randn((M, K), device="cuda", generator=g).half()
+    W = torch.randn((N, K), device="cuda", generator=g)
+    q, s = Q.qgemm_mx_quantize_device(W)
+    w = Q.qgemm_mx_dequantize_device(q, s).double()
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, q, s)
+    C = torch.full((M, N), float("nan"), device="cuda")
+    Q.qgemm_run_ex(M, K, N, fmt, A, Bq, Sp, C)
+    a = Q.qgemm_mx_dequantize_device(*Q.qgemm_mx_quantize_device(A)).double() if fmt == "mxfp4a4" else A.double()
+    ref, mass = a @ w.t(), a.abs() @ w.abs().t()
+    err = (C.double() - ref).abs()
+    assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 1e-37).all())
+    assert float(err.norm()) <= 4 * (K + 16) ** 0.5 * 2.0 ** -24 * float(mass.norm())
