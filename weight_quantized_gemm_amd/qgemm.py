@@ -435,18 +435,19 @@ _TYPE_IDS = {d: t for t, d in _TORCH_TYPES.items()}
 def _same_device(**tensors):
     """Checks that the tensors (None passes) are GPU tensors of one device and
     returns it."""
-    dev = None
+    first, index = None, -1
     for name, t in tensors.items():
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        i = t.get_device() if isinstance(t, torch.Tensor) else -1      # -1: on the host
+        if i == index >= 0:
+            continue
+        if i < 0:
             raise ValueError(f"{name}: expected a GPU tensor")
-        d = t.device
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{name}: on {d}, the other tensors on {dev}")
-    return dev
+        if first is not None:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {first.device}")
+        first, index = t, i
+    return None if first is None else first.device
 
 
 def _exact(t, name: str, dtypes, shape):
