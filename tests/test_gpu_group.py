@@ -443,3 +443,29 @@ def test_every_tile_of_the_grouped_product(fmt, mean, K):
         err = (C[lo:hi].double() - ref).abs()
         assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 1e-37).all()), e
     assert bool((C[n:] == 9.0).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_layer_on_a_given_stream(fmt):
+    """Every call with stream= and no workspace: the library's own stream-ordered
+    scratch, the same bits."""
+    T, topk, E, K, N = 3000, 3, 8, 512, 384
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(0, E + 2, (T, topk), device="cuda", generator=g, dtype=torch.int32)
+    wt = torch.rand((T, topk), device="cuda", generator=g)
+    A = torch.randn((T, K), device="cuda", generator=g).half()
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, *Q.qgemm_mx_quantize_device(
+        torch.randn((E * N, K), device="cuda", generator=g)), E=E)
+
+    def layer(stream):
+        C, out = torch.zeros((T * topk, N), device="cuda"), torch.empty((T, N), device="cuda")
+        torch.cuda.synchronize()
+        offsets, rows, slots = Q.qgemm_group_plan(ids, E, stream=stream)
+        Q.qgemm_run_grouped(K, N, E, fmt, A, rows, offsets, Bq, Sp, C, activation="relu", stream=stream)
+        Q.qgemm_group_combine(C, slots, wt, out, stream=stream)
+        torch.cuda.synchronize()
+        return out
+
+    want, side = layer(None), torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        assert torch.equal(layer(stream), want)

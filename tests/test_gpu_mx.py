@@ -334,3 +334,24 @@ def test_every_tile_with_stages_left_over(fmt, M, N, K):
     err = (C.double() - ref).abs()
     assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 1e-37).all())
     assert float(err.norm()) <= 4 * (K + 16) ** 0.5 * 2.0 ** -24 * float(mass.norm())
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 512, 33), (6, 576, 64), (20, 832, 130), (40, 1024, 18500), (300, 640, 257)])
+@pytest.mark.parametrize("out", ["f32", "f16"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_residual_in_place(fmt, M, K, N, out):
+    """The residual may be C itself: the same bits as from a copy of it, dense
+    and as one group of a grouped product."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    A = torch.randn((M, K), device="cuda", generator=g).half()
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, *Q.qgemm_mx_quantize_device(torch.randn((N, K), device="cuda", generator=g)))
+    R = torch.randn((M, N), device="cuda", generator=g).to(torch.float16 if out == "f16" else torch.float32)
+    want, C = torch.empty_like(R), R.clone()
+    Q.qgemm_run_ex(M, K, N, fmt, A, Bq, Sp, want, residual=R, activation="silu", out_type=out)
+    Q.qgemm_run_ex(M, K, N, fmt, A, Bq, Sp, C, residual=C, activation="silu", out_type=out)
+    assert torch.equal(C, want)
+    offsets = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    want, C = torch.empty_like(R), R.clone()
+    Q.qgemm_run_grouped(K, N, 1, fmt, A, None, offsets, Bq, Sp, want, residual=R, activation="silu", out_type=out)
+    Q.qgemm_run_grouped(K, N, 1, fmt, A, None, offsets, Bq, Sp, C, residual=C, activation="silu", out_type=out)
+    assert torch.equal(C, want)
