@@ -355,3 +355,43 @@ def test_residual_in_place(fmt, M, K, N, out):
     Q.qgemm_run_grouped(K, N, 1, fmt, A, None, offsets, Bq, Sp, want, residual=R, activation="silu", out_type=out)
     Q.qgemm_run_grouped(K, N, 1, fmt, A, None, offsets, Bq, Sp, C, residual=C, activation="silu", out_type=out)
     assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(12, 6144, 100), (33, 9728, 2560), (100, 8192, 1001), (250, 9728, 2560),
+                                   (500, 9728, 2560), (17, 16384, 1024), (200, 16448, 640)])
+def test_split_k(M, K, N):
+    """Few tiles and a long K: K in slices, added in their order (the same bits
+    every time), with every epilogue, through each entry point and its own
+    scratch. (500 rows make enough tiles to stay whole: the same checks.)"""
+    assert Q.qgemm_workspace_size(M, K, N, "mxfp4") >= (2 * M * N * 4 if M < 500 else 0)
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    A = torch.randn((M, K), device="cuda", generator=g).half()
+    q, s = Q.qgemm_mx_quantize_device(torch.randn((N, K), device="cuda", generator=g))
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, q, s)
+    w = Q.qgemm_mx_dequantize_device(q, s).double()
+    bias = torch.randn(N, device="cuda", generator=g)
+    res = torch.randn((M, N), device="cuda", generator=g).half()
+    ref, mass = A.double() @ w.t(), A.double().abs() @ w.abs().t()
+    bound = (K + 16) * 2.0 ** -23 * mass + 1e-37
+    C = torch.full((M, N), float("nan"), device="cuda")
+    Q.qgemm_run(M, K, N, "mxfp4", A, Bq, Sp, C)
+    assert bool(((C.double() - ref).abs() <= bound).all())
+    assert float((C.double() - ref).norm()) <= 4 * (K + 16) ** 0.5 * 2.0 ** -24 * float(mass.norm())
+    nb = Q.qgemm_workspace_size(M, K, N, "mxfp4")
+    ws = torch.full((max(nb, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        D = torch.full((M, N), float("nan"), device="cuda")
+        Q.qgemm_run_ws(M, K, N, "mxfp4", A, Bq, Sp, D, ws, nb)
+        assert torch.equal(C, D)
+    if nb <= Q.NOALLOC_SCRATCH_BYTES:
+        D = torch.full((M, N), float("nan"), device="cuda")
+        Q.qgemm_run_noalloc(M, K, N, "mxfp4", A, Bq, Sp, D)
+        assert torch.equal(C, D)
+    # relu has slope 1; an fp16 result rounds by half a step
+    H = res.clone()
+    Q.qgemm_run_ex(M, K, N, "mxfp4", A, Bq, Sp, H, bias=bias, residual=H, activation="relu", out_type="f16",
+                   workspace=ws, ws_bytes=nb)
+    full = (ref + bias.double() + res.double()).clamp(min=0)
+    err = (H.double() - full).abs()
+    assert bool((err <= bound + (K + 16) * 2.0 ** -23 * (bias.abs().double() + res.abs().double())
+                 + 2.0 ** -11 * full + 2.0 ** -25).all())

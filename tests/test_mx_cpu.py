@@ -239,3 +239,16 @@ def test_binding_refuses_host_tensors():
         Q.qgemm_group_combine(x, i, x[:, :2].contiguous(), x)
     with pytest.raises(ValueError):
         Q.qgemm_run_grouped(64, 32, 2, "mxfp4", x.half(), None, i, i, i, x)
+
+
+def test_split_k_scratch():
+    """Few tiles and a long K take partial tiles (fp32, whole slices); enough
+    tiles, a short K, and MXFP4 activations do not."""
+    for M, K, N in ((32, 9728, 2560), (256, 9728, 2560), (17, 16384, 1024), (12, 6144, 100)):
+        need = Q.qgemm_workspace_size(M, K, N, "mxfp4")
+        part = M * N * 4
+        assert 2 * part <= need < 8 * part + 256
+        codes = M * (-(-K // 256)) * 128
+        assert codes <= Q.qgemm_workspace_size(M, K, N, "mxfp4a4") < codes + M * (K // 256 + 8) * 8 + 512
+    for M, K, N in ((64, 4096, 4096), (32, 1024, 64), (2048, 9728, 2560), (512, 4096, 4096), (1, 64, 1)):
+        assert Q.qgemm_workspace_size(M, K, N, "mxfp4") == 0

@@ -195,8 +195,8 @@ static qgemm_status dispatch(int M, int K, int N, qgemm_format f, const Geometry
     case QGEMM_MXFP4_A4:
         return launched(launch_mx_gemm(f, MxArgs{M, M, K, N, 1, A, nullptr, nullptr,
                                                  static_cast<const uint8_t *>(Bq),
-                                                 static_cast<const uint8_t *>(scales), 0, 0, C, epi, nullptr,
-                                                 nullptr, 0},
+                                                 static_cast<const uint8_t *>(scales), 0, 0, C, epi, nsplit, part,
+                                                 nullptr, nullptr, 0},
                                        gemv, ws, s));
     default:
         break;
@@ -558,7 +558,7 @@ qgemm_status qgemm_run_grouped(int S, int a_rows, int K, int N, int E, qgemm_for
     hipStream_t s = static_cast<hipStream_t>(stream);
     const MxArgs args{S, a_rows, K, N, E, A, rows, offsets,
                       static_cast<const uint8_t *>(Bq), static_cast<const uint8_t *>(scales), g.w_bytes, g.s_bytes,
-                      C, epi, nullptr, nullptr, 0};
+                      C, epi, 1, nullptr, nullptr, nullptr, 0};
     return with_scratch(need, workspace, ws_bytes, s,
                         [&](void *ws) { return launched(launch_mx_gemm(f, args, decode, ws, s)); });
 }

@@ -138,6 +138,63 @@ long long mx_grid(int S, int E, int N) {
     return (groups + (S - groups) / 8) * div_up(N, 32) + 7;
 }
 
+// All rows in whole tiles, and half a tile more for every group that has rows
+// (with S slots dealt evenly, about S E / (S + E) groups); at least one tile
+// each.
+long long mx_expect_tiles(MxShape t, int S, int E, int N) {
+    const int bm = kMxTileRows[t];
+    long long rows = div_up(S, bm);
+    if (E > 1) {
+        const long long some = (long long)S * E / ((long long)S + E) + 1;
+        rows = S / bm + some / 2 > some ? S / bm + some / 2 : some;
+    }
+    return rows * div_up(N, kMxTileCols[t]);
+}
+
+// Measurements: beside the kernels.
+static MxShape mx_dense_shape(bool A4, int M, int N) {
+    auto enough = [&](MxShape t, int n) { return mx_expect_tiles(t, M, 1, N) >= n; };
+    if (M > (A4 ? 96 : 384) && enough(T128x256, A4 ? kMxEnoughTiles : 512)) return T128x256;
+    if (M > 48 && enough(T64x256, 256)) return T64x256;
+    if (M > 32 && enough(T64x128, kMxEnoughTiles)) return T64x128;
+    return enough(T32x64, kMxEnoughTiles) ? T32x64 : T32x32;
+}
+
+// Splitting K pays where the tiles are few and K is long: a workgroup is then
+// bound by the bytes it brings into its CU (2 a row and 17/32 a column of its
+// tile for every K-element), a split divides them over the CUs that have no
+// tile, and larger tiles, too few by themselves, need fewer bytes for each
+// output. It costs a second launch and the partial tiles, written and read
+// once. Estimated time, fitted to 21 shapes with M = 16 to 512 (us; the plan's
+// choices are 2 % above the best of all tiles and slices there on average): a
+// round of tiles takes its bytes at 75 GB/s and 4 bytes an output at 20 GB/s;
+// a split 3 and its partial tiles at 3 TB/s. Measured, unsplit -> split: 32 x
+// 9728 x 2560 12.9 -> 10.6 (32 x 64 tiles), 256 x 9728 x 2560 26.9 -> 21.3 (64
+// x 128, three slices), 32 x 16384 x 1024 17.2 -> 11.1; not 64 x 4096 x 4096
+// (8.3 -> 9.8), 32 x 4096 x 1024 (8.0 -> 8.2). MXFP4 activations, a quarter
+// of the bytes a row, gain nothing (32 x 9728 x 2560 11.1 -> 11.7).
+MxPlan mx_dense_plan(bool A4, int M, int K, int N) {
+    MxPlan best{mx_dense_shape(A4, M, N), 1};
+    if (A4 || best.shape == T128x256 || best.shape == T64x256) return best;
+    auto loop = [&](MxShape t, int slices) {
+        const long long rounds = (mx_expect_tiles(t, M, 1, N) * slices + kSplitTargetCUs - 1) / kSplitTargetCUs;
+        return rounds * ((K / slices) * (2 * kMxTileRows[t] + 0.53125 * kMxTileCols[t]) / 75e3 +
+                         4 * kMxTileRows[t] * kMxTileCols[t] / 20e3);
+    };
+    double best_us = loop(best.shape, 1);
+    for (const MxShape t : {T32x32, T32x64, T32x128, T64x128, T64x256}) {
+        const long long tiles = mx_expect_tiles(t, M, 1, N);
+        for (int sp = 2; sp <= kMaxSplit && sp * tiles <= kSplitTargetCUs && K / sp >= 1024; ++sp) {
+            const double us = loop(t, sp) + 3.0 + (2 * sp + 1) * (4.0 * M * N) / 3e6;
+            if (us < best_us) {
+                best = MxPlan{t, sp};
+                best_us = us;
+            }
+        }
+    }
+    return best;
+}
+
 int f32_kgroups(int M, int N) {
     const long long tiles = (long long)div_up(M, M <= kF32TileMSmall ? kF32TileMSmall : kF32TileM) *
                             div_up(N, kF32TileN);
@@ -146,6 +203,7 @@ int f32_kgroups(int M, int N) {
 
 int splitk_plan(qgemm_format f, int M, int K, int N) {
     if (M <= 0 || N <= 0 || K <= 0) return 1;
+    if (is_mx(f)) return mx_dense_plan(f == QGEMM_MXFP4_A4, M, K, N).nsplit;
     f = kernel_format(f);
     long long tiles = 0;
     int kunits = 0;                  // K granules: the most slices a split may have

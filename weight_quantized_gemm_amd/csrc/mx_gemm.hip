@@ -286,8 +286,9 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     // (of whole pairs with MXFP4 activations, whose scales come in pairs)
     constexpr int U = A4 ? 2 : 1;
     const int units = (nall + U - 1) / U;
-    const int st0 = U * (kg * units / WK), nst = min(U * ((kg + 1) * units / WK), nall) - st0;
-    const int nmax = U * ((units + WK - 1) / WK);      // of the longest K group, at most
+    const int G = WK * (int)gridDim.y, g = WK * (int)blockIdx.y + kg;     // K groups of all slices, this one
+    const int st0 = U * (g * units / G), nst = min(U * ((g + 1) * units / G), nall) - st0;
+    const int nmax = U * ((units + G - 1) / G);      // of the longest K group, at most
     const int last = max(nst - 1, 0);
 
     // A: gathered rows from the array's start, others from the tile's first row
@@ -518,6 +519,8 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     __builtin_amdgcn_s_waitcnt(vm_wait(0));      // no DMA in flight into what follows
     __syncthreads();
     float *const out = reinterpret_cast<float *>(lds);
+    // (slice y of a split K: its partial tiles; one slice is C itself)
+    void *const C = static_cast<float *>(p.C) + (size_t)blockIdx.y * p.S * p.N;
     auto store = [&](auto vec) {
         using CE = ColumnEpilogue<decltype(vec)::value>;
         if constexpr (WK > 1) {
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
             constexpr int TPR = T::BN / 4, STEP = T::THREADS / TPR;      // threads per row, rows per turn
             static_assert(T::THREADS % TPR == 0, "a thread keeps its columns");
             const int col = 4 * (threadIdx.x % TPR);
-            const CE ce(epi, p.C, n0 + col, p.N);
+            const CE ce(epi, C, n0 + col, p.N);
             const float *src = out + (threadIdx.x / TPR) * T::BN + col;
 #pragma unroll 1
             for (int m = threadIdx.x / TPR; m < rt.n; m += STEP, src += STEP * T::BN) {
@@ -539,7 +542,7 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
             constexpr int LPR = 8 * CF, STEP = 64 / LPR;      // lanes per row, rows per turn
             float *const own = out + wave * 32 * T::PITCH;
             const int col = 4 * (lane % LPR);
-            const CE ce(epi, p.C, n0 + 32 * CF * wn + col, p.N);
+            const CE ce(epi, C, n0 + 32 * CF * wn + col, p.N);
 #pragma unroll
             for (int rf = 0; rf < RF; ++rf) {
                 const int m0 = 32 * (RF * wm + rf);
@@ -732,34 +735,11 @@ namespace {
 //   8                        38.4        34.8        31.2        31.9        61.7
 //   1                        18.6        16.3        15.8        16.0        18.5
 // One token's 8 of 64 experts of 2560 x 2048: 8 rows (decode) 8.2, 2 rows 7.9.
+// Split K (dense, few tiles) multiplies the workgroups by the slices of K; a
+// second launch adds the slices up in their order and applies the epilogue.
 // ---------------------------------------------------------------------------
-enum Shape { T128x256, T64x256, T64x128, T32x256, T32x128, T32x64, T32x32 };
-constexpr int kTileRows[] = {128, 64, 64, 32, 32, 32, 32}, kTileCols[] = {256, 256, 128, 256, 128, 64, 32};
-constexpr int kEnoughTiles = 144;       // of 256 CUs: from here a larger tile beats more workgroups
-
-// Tiles to expect of S slots in E groups: all their rows in whole tiles, and
-// half a tile more for every group that has rows (with S slots dealt evenly,
-// about S E / (S + E) groups); at least one tile each.
-long long expect_tiles(Shape t, int S, int E, int N) {
-    const int bm = kTileRows[t];
-    long long rows = div_up(S, bm);
-    if (E > 1) {
-        const long long some = (long long)S * E / ((long long)S + E) + 1;
-        rows = S / bm + some / 2 > some ? S / bm + some / 2 : some;
-    }
-    return rows * div_up(N, kTileCols[t]);
-}
-
-Shape dense_shape(bool A4, int M, int N) {
-    auto enough = [&](Shape t, int n) { return expect_tiles(t, M, 1, N) >= n; };
-    if (M > (A4 ? 96 : 384) && enough(T128x256, A4 ? kEnoughTiles : 512)) return T128x256;
-    if (M > 48 && enough(T64x256, 256)) return T64x256;
-    if (M > 32 && enough(T64x128, kEnoughTiles)) return T64x128;
-    return enough(T32x64, kEnoughTiles) ? T32x64 : T32x32;
-}
-
-Shape grouped_shape(bool A4, int S, int E, int N) {
-    auto enough = [&](Shape t) { return expect_tiles(t, S, E, N) >= kEnoughTiles; };
+MxShape grouped_shape(bool A4, int S, int E, int N) {
+    auto enough = [&](MxShape t) { return mx_expect_tiles(t, S, E, N) >= kMxEnoughTiles; };
     const int rows = S / (S < E ? S : E);      // of the average group
     if (A4 && rows >= 128 && enough(T128x256)) return T128x256;
     if (rows >= (A4 ? 12 : 24) && enough(T64x256)) return T64x256;
@@ -779,7 +759,8 @@ template <class T>
 hipError_t launch_tile(MxArgs p, hipStream_t s) {
     p.tiles_n = div_up(p.N, T::BN);
     const long long grid = most_row_tiles(p.S, p.offsets ? p.E : 1, T::BM) * p.tiles_n;
-    hipLaunchKernelGGL(mx_tile_kernel<T>, dim3((unsigned)((grid + 7) / 8 * 8)), dim3(T::THREADS), 0, s, p);
+    hipLaunchKernelGGL(mx_tile_kernel<T>, dim3((unsigned)((grid + 7) / 8 * 8), (unsigned)p.nsplit), dim3(T::THREADS), 0,
+                       s, p);
     return hipGetLastError();
 }
 
@@ -801,8 +782,8 @@ hipError_t launch_decode(const MxArgs &p, hipStream_t s) {
 }
 
 template <bool A4>
-hipError_t launch_tiles(const MxArgs &p, hipStream_t s) {
-    switch (p.offsets ? grouped_shape(A4, p.S, p.E, p.N) : dense_shape(A4, p.S, p.N)) {
+hipError_t launch_shape(MxShape shape, const MxArgs &p, hipStream_t s) {
+    switch (shape) {
     //                                       RF CF WM WN WK NS BR waves a SIMD
     case T128x256: return launch_tile<Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
     case T64x256:  return launch_tile<Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
@@ -814,11 +795,25 @@ hipError_t launch_tiles(const MxArgs &p, hipStream_t s) {
     }
 }
 
+template <bool A4>
+hipError_t launch_tiles(const MxArgs &args, hipStream_t s) {
+    if (args.nsplit > 1) {
+        MxArgs p = args;
+        p.C = args.part;
+        p.epi = Epilogue{nullptr, nullptr, QGEMM_ACT_NONE, 0, true};
+        const hipError_t e = launch_shape<A4>(mx_dense_plan(A4, p.S, p.K, p.N).shape, p, s);
+        return e != hipSuccess ? e : launch_splitk_reduce_f32(args.part, args.nsplit, p.S, p.N, args.C, args.epi, s);
+    }
+    return launch_shape<A4>(args.offsets ? grouped_shape(A4, args.S, args.E, args.N)
+                                         : mx_dense_plan(A4, args.S, args.K, args.N).shape,
+                            args, s);
+}
+
 }  // namespace
 
 // Few rows a group and too few 32 x 128 tiles to fill the CUs.
 bool mx_grouped_decode(int S, int E, int N) {
-    return S / (S < E ? S : E) <= 2 && expect_tiles(T32x128, S, E, N) < kEnoughTiles;
+    return S / (S < E ? S : E) <= 2 && mx_expect_tiles(T32x128, S, E, N) < kMxEnoughTiles;
 }
 
 hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, bool decode, void *ws, hipStream_t s) {

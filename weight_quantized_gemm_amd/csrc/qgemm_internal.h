@@ -298,6 +298,8 @@ struct MxArgs {
     size_t w_bytes, s_bytes;          // from one group's to the next
     void *C;
     Epilogue epi;
+    int nsplit;                       // slices of K (the dense tiled product's; else 1) and their partial
+    float *part;                      // tiles, fp32 [nsplit][S][N], where there are two or more
     // set by the launcher
     const uint8_t *Aq, *As;           // MXFP4_A4: activation codes [a_rows][Kp / 2] and
                                       // scales (mx_act_scale), Kp = roundup(K, 256)
@@ -310,6 +312,18 @@ struct MxWorkspace {
 MxWorkspace mx_workspace(qgemm_format f, long long rows, int K);
 // Workgroups of the product's launch, at most (2^31 - 1 are allowed).
 long long mx_grid(int S, int E, int N);
+// Tiles of the tiled product (rows x columns).
+enum MxShape { T128x256, T64x256, T64x128, T32x256, T32x128, T32x64, T32x32 };
+constexpr int kMxEnoughTiles = 144;     // of 256 CUs: from here a larger tile beats more workgroups
+constexpr int kMxTileRows[] = {128, 64, 64, 32, 32, 32, 32}, kMxTileCols[] = {256, 256, 128, 256, 128, 64, 32};
+// Tiles to expect of S slots in E groups.
+long long mx_expect_tiles(MxShape t, int S, int E, int N);
+// The dense product's tile, and slices of K; a function of the shape alone.
+struct MxPlan {
+    MxShape shape;
+    int nsplit;
+};
+MxPlan mx_dense_plan(bool A4, int M, int K, int N);
 // decode: the kernel for few rows, which needs no scratch; for the dense product
 // up to the GEMV limit's rows, for a grouped one as mx_grouped_decode says.
 bool mx_grouped_decode(int S, int E, int N);
