@@ -151,41 +151,41 @@ long long mx_expect_tiles(MxShape t, int S, int E, int N) {
     return rows * div_up(N, kMxTileCols[t]);
 }
 
-// Measurements: beside the kernels.
-static MxShape mx_dense_shape(bool A4, int M, int N) {
-    auto enough = [&](MxShape t, int n) { return mx_expect_tiles(t, M, 1, N) >= n; };
-    if (M > (A4 ? 96 : 384) && enough(T128x256, A4 ? kMxEnoughTiles : 512)) return T128x256;
-    if (M > 48 && enough(T64x256, 256)) return T64x256;
-    if (M > 32 && enough(T64x128, kMxEnoughTiles)) return T64x128;
-    return enough(T32x64, kMxEnoughTiles) ? T32x64 : T32x32;
-}
-
-// Splitting K pays where the tiles are few and K is long: a workgroup is then
-// bound by the bytes it brings into its CU (2 a row and 17/32 a column of its
-// tile for every K-element), a split divides them over the CUs that have no
-// tile, and larger tiles, too few by themselves, need fewer bytes for each
-// output. It costs a second launch and the partial tiles, written and read
-// once. Estimated time, fitted to 21 shapes with M = 16 to 512 (us; the plan's
-// choices are 2 % above the best of all tiles and slices there on average): a
-// round of tiles takes its bytes at 75 GB/s and 4 bytes an output at 20 GB/s;
-// a split 3 and its partial tiles at 3 TB/s. Measured, unsplit -> split: 32 x
-// 9728 x 2560 12.9 -> 10.6 (32 x 64 tiles), 256 x 9728 x 2560 26.9 -> 21.3 (64
-// x 128, three slices), 32 x 16384 x 1024 17.2 -> 11.1; not 64 x 4096 x 4096
-// (8.3 -> 9.8), 32 x 4096 x 1024 (8.0 -> 8.2). MXFP4 activations, a quarter
-// of the bytes a row, gain nothing (32 x 9728 x 2560 11.1 -> 11.7).
+// Large tiles where they are enough (measurements beside the kernels), and
+// with MXFP4 activations the smaller ones likewise.
+//
+// With fp16 activations a workgroup of the smaller tiles is bound by the bytes
+// it brings into its CU: 2 a row and 17/32 a column of its tile for every
+// K-element. Where tiles are few and K is long, a split of K divides them over
+// the CUs that have no tile, and larger tiles, too few by themselves, need
+// fewer bytes for each output; it costs a second launch and the partial tiles,
+// written and read once. Estimated time (us): a round of tiles takes its bytes
+// at 75 GB/s and 4 bytes an output at 6.8 GB/s; a split 2.2 and its partial
+// tiles at 5.5 TB/s. Fitted to 43 shapes with M = 10 to 512: the choices are 1 %
+// above the best of all tiles and slices there on average, 17 % at most.
+// Measured, tile by count alone -> by estimate: 32 x 9728 x 2560 12.9 -> 10.8
+// (32 x 64, six slices), 256 x 9728 x 2560 30.6 -> 22.0 (64 x 128, three), 32 x
+// 16384 x 1024 17.2 -> 11.1, 400 x 6144 x 2560 26.7 -> 20.8 (64 x 128, whole),
+// 256 x 4096 x 4096 14.5 -> 13.7 (32 x 128, whole); whole stay 64 x 4096 x 4096
+// (8.3, in two slices 9.8) and 32 x 4096 x 1024 (8.0, 8.2). With MXFP4
+// activations, a quarter of the bytes a row, no split gained (32 x 9728 x 2560
+// 11.1 -> 11.7).
 MxPlan mx_dense_plan(bool A4, int M, int K, int N) {
-    MxPlan best{mx_dense_shape(A4, M, N), 1};
-    if (A4 || best.shape == T128x256 || best.shape == T64x256) return best;
-    auto loop = [&](MxShape t, int slices) {
-        const long long rounds = (mx_expect_tiles(t, M, 1, N) * slices + kSplitTargetCUs - 1) / kSplitTargetCUs;
-        return rounds * ((K / slices) * (2 * kMxTileRows[t] + 0.53125 * kMxTileCols[t]) / 75e3 +
-                         4 * kMxTileRows[t] * kMxTileCols[t] / 20e3);
-    };
-    double best_us = loop(best.shape, 1);
+    auto tiles = [&](MxShape t) { return mx_expect_tiles(t, M, 1, N); };
+    if (M > (A4 ? 96 : 384) && tiles(T128x256) >= (A4 ? kMxEnoughTiles : 512)) return MxPlan{T128x256, 1};
+    if (M > 48 && tiles(T64x256) >= 256) return MxPlan{T64x256, 1};
+    if (A4) {
+        if (M > 32 && tiles(T64x128) >= kMxEnoughTiles) return MxPlan{T64x128, 1};
+        return MxPlan{tiles(T32x64) >= kMxEnoughTiles ? T32x64 : T32x32, 1};
+    }
+    MxPlan best{T32x32, 1};
+    double best_us = 1e30;
     for (const MxShape t : {T32x32, T32x64, T32x128, T64x128, T64x256}) {
-        const long long tiles = mx_expect_tiles(t, M, 1, N);
-        for (int sp = 2; sp <= kMaxSplit && sp * tiles <= kSplitTargetCUs && K / sp >= 1024; ++sp) {
-            const double us = loop(t, sp) + 3.0 + (2 * sp + 1) * (4.0 * M * N) / 3e6;
+        const double fill = 2 * kMxTileRows[t] + 0.53125 * kMxTileCols[t];
+        for (int sp = 1; sp == 1 || (sp <= kMaxSplit && sp * tiles(t) <= kSplitTargetCUs && K / sp >= 1024); ++sp) {
+            const long long rounds = (sp * tiles(t) + kSplitTargetCUs - 1) / kSplitTargetCUs;
+            const double us = rounds * (K / sp * fill / 75e3 + 4 * kMxTileRows[t] * kMxTileCols[t] / 6.8e3) +
+                              (sp > 1 ? 2.2 + (2 * sp + 1) * (4.0 * M * N) / 5.5e6 : 0);
             if (us < best_us) {
                 best = MxPlan{t, sp};
                 best_us = us;
