@@ -734,19 +734,24 @@ namespace {
 //   16                       41.5        35.9        36.9        37.4
 //   8                        38.4        34.8        31.2        31.9        61.7
 //   1                        18.6        16.3        15.8        16.0        18.5
+// 32 x 256 tiles, one K group of four waves each, need two on a CU: 800 rows
+// over 64 experts of 2560 x 640, 180 such tiles 24.1, 300 of 32 x 128 17.5 (18.0
+// and 16.6 with MXFP4 activations); 300 rows over 16 of 9728 x 2560 73.5
+// [170], 57.6. Over 37 layers of 2 to 256 experts the rules' choice is 2 %
+// (MXFP4 activations: 1 %) above the best tile on average, 24 % at most.
 // One token's 8 of 64 experts of 2560 x 2048: 8 rows (decode) 8.2, 2 rows 7.9.
 // Split K (dense, few tiles) multiplies the workgroups by the slices of K; a
 // second launch adds the slices up in their order and applies the epilogue.
 // ---------------------------------------------------------------------------
 MxShape grouped_shape(bool A4, int S, int E, int N) {
-    auto enough = [&](MxShape t) { return mx_expect_tiles(t, S, E, N) >= kMxEnoughTiles; };
+    auto tiles = [&](MxShape t) { return mx_expect_tiles(t, S, E, N); };
     const int rows = S / (S < E ? S : E);      // of the average group
-    if (A4 && rows >= 128 && enough(T128x256)) return T128x256;
-    if (rows >= (A4 ? 12 : 24) && enough(T64x256)) return T64x256;
-    if (rows >= 24 && enough(T64x128)) return T64x128;
-    if (rows >= (A4 ? 1 : 6) && enough(T32x256)) return T32x256;
-    if (enough(T32x128)) return T32x128;
-    return enough(T32x64) ? T32x64 : T32x32;
+    if (A4 && rows >= 128 && tiles(T128x256) >= kMxEnoughTiles) return T128x256;
+    if (rows >= 24 && tiles(T64x256) >= kMxEnoughTiles) return T64x256;
+    if (rows >= 24 && tiles(T64x128) >= kMxEnoughTiles) return T64x128;
+    if (rows >= (A4 ? 1 : 6) && tiles(T32x256) >= kSplitTargetCUs) return T32x256;
+    if (tiles(T32x128) >= kMxEnoughTiles) return T32x128;
+    return tiles(T32x64) >= kMxEnoughTiles ? T32x64 : T32x32;
 }
 
 // The most row tiles of `rows` rows that S slots in E groups can make.
