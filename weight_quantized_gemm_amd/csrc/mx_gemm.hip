@@ -281,14 +281,17 @@ __global__ __launch_bounds__(T::THREADS, T::MINW) void mx_tile_kernel(MxArgs p) 
     rt = RowTile{uniform(rt.e), uniform(rt.s0), uniform(rt.n), uniform(rt.tn)};
     const int tn = rt.tn;
     const int n64 = p.K >> 6, n256 = (p.K + 255) >> 8;
-    // this K group's stages
+    // this slice's stages, and of those this K group's
     const int nall = A4 ? n256 : n64;
     // (of whole pairs with MXFP4 activations, whose scales come in pairs)
     constexpr int U = A4 ? 2 : 1;
-    const int units = (nall + U - 1) / U;
-    const int G = WK * (int)gridDim.y, g = WK * (int)blockIdx.y + kg;     // K groups of all slices, this one
-    const int st0 = U * (g * units / G), nst = min(U * ((g + 1) * units / G), nall) - st0;
-    const int nmax = U * ((units + G - 1) / G);      // of the longest K group, at most
+    int lo = 0, units = (nall + U - 1) / U;
+    if (gridDim.y > 1) {
+        lo = (int)blockIdx.y * units / (int)gridDim.y;
+        units = ((int)blockIdx.y + 1) * units / (int)gridDim.y - lo;
+    }
+    const int st0 = U * (lo + kg * units / WK), nst = min(U * (lo + (kg + 1) * units / WK), nall) - st0;
+    const int nmax = U * ((units + WK - 1) / WK);      // of the longest K group, at most
     const int last = max(nst - 1, 0);
 
     // A: gathered rows from the array's start, others from the tile's first row
