@@ -469,3 +469,43 @@ def test_layer_on_a_given_stream(fmt):
     want, side = layer(None), torch.cuda.Stream()
     for stream in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
         assert torch.equal(layer(stream), want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_two_threads_on_one_stream(fmt):
+    """Two threads of a program on the same stream, neither giving a workspace
+    nor outputs of the plan: each gets what it gets alone."""
+    import threading
+    T, topk, E, K, N = 3000, 2, 8, 512, 256
+    sets = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids = torch.randint(0, E + 1, (T, topk), device="cuda", generator=g, dtype=torch.int32)
+        A = torch.randn((T, K), device="cuda", generator=g).half()
+        Bq, Sp = Q.qgemm_mx_pack_device(K, N, *Q.qgemm_mx_quantize_device(
+            torch.randn((E * N, K), device="cuda", generator=g)), E=E)
+        sets.append((ids, A, Bq, Sp))
+
+    def layer(ids, A, Bq, Sp):
+        C = torch.zeros((T * topk, N), device="cuda")
+        offsets, rows, slots = Q.qgemm_group_plan(ids, E)
+        Q.qgemm_run_grouped(K, N, E, fmt, A, rows, offsets, Bq, Sp, C)
+        return offsets, rows, slots, C
+
+    want = [layer(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(40):
+            got[i].append(layer(*sets[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert len(runs) == 40
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(w, r))

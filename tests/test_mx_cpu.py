@@ -252,3 +252,39 @@ def test_split_k_scratch():
         assert codes <= Q.qgemm_workspace_size(M, K, N, "mxfp4a4") < codes + M * (K // 256 + 8) * 8 + 512
     for M, K, N in ((64, 4096, 4096), (32, 1024, 64), (2048, 9728, 2560), (512, 4096, 4096), (1, 64, 1)):
         assert Q.qgemm_workspace_size(M, K, N, "mxfp4") == 0
+
+
+@pytest.mark.parametrize("call", ["plan", "grouped"])
+def test_scratch_lives_until_the_call_returns(call, monkeypatch):
+    """Scratch that the binding takes itself is held while the library enqueues
+    its launches: freed before, another thread's call on the same stream gets
+    the same memory between two of them."""
+    import weakref
+
+    import torch
+    made, seen = [], []
+    empty = torch.empty
+
+    def spy(*a, **kw):
+        t = empty(*a, **kw)
+        made.append((weakref.ref(t), t.data_ptr(), t.numel() * t.element_size()))
+        return t
+
+    def enqueue(name, dev, stream, *args):
+        ws, n = args[-2:]
+        seen.append(name)
+        assert any(ref() is not None and p == ws and b >= n > 0 for ref, p, b in made), "scratch was given back"
+
+    monkeypatch.setattr(torch, "empty", spy)
+    monkeypatch.setattr(Q, "_same_device", lambda **t: torch.device("cpu"))
+    monkeypatch.setattr(Q, "_call", enqueue)
+    if call == "plan":
+        Q.qgemm_group_plan(torch.zeros((4096, 2), dtype=torch.int32), 8)
+    else:
+        monkeypatch.setattr(Q, "_dev_ptr", lambda t: None if t is None else t.data_ptr())
+        K, N, E, S = 64, 32, 2, 800
+        wb, sb = Q.qgemm_packed_size(K, N, "mxfp4a4")
+        Q.qgemm_run_grouped(K, N, E, "mxfp4a4", torch.zeros((S, K), dtype=torch.float16), None,
+                            torch.zeros(E + 1, dtype=torch.int32), torch.zeros(E * wb, dtype=torch.uint8),
+                            torch.zeros(E * sb, dtype=torch.uint8), torch.zeros((S, N)))
+    assert len(seen) == 1

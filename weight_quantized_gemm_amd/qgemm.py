@@ -602,15 +602,19 @@ def _scratch(workspace, ws_bytes: int):
 
 
 def _own_scratch(need: int, workspace, ws_bytes: int, dev, stream):
-    """(address, bytes) of a call's scratch: the caller's, or one from torch's
-    allocator, which hands its memory out and takes it back in the order of the
-    current stream at next to no cost. For a call on another stream that order
-    says nothing, so the library allocates on that stream itself."""
+    """(tensor, address, bytes) of a call's scratch: the caller's, or one from
+    torch's allocator, which hands its memory out and takes it back in the order
+    of the current stream at next to no cost. The caller holds the tensor until
+    the library has enqueued every launch of the call: given back before, its
+    memory could go to another thread's work on the same stream between two of
+    them. For a call on another stream that order says nothing, so the library
+    allocates on that stream itself."""
     if workspace is not None:
-        return _scratch(workspace, ws_bytes), ws_bytes
+        return workspace, _scratch(workspace, ws_bytes), ws_bytes
     if need == 0 or ws_bytes or stream is not None:
-        return None, ws_bytes
-    return torch.empty(need, dtype=torch.uint8, device=dev).data_ptr(), need
+        return None, None, ws_bytes
+    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    return scratch, scratch.data_ptr(), need
 
 
 def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace=None, ws_bytes: int = 0,
@@ -636,9 +640,10 @@ def qgemm_group_plan(ids, E: int, offsets=None, rows=None, slots=None, workspace
         slots = _empty((T, topk), torch.int32, dev, stream)
     else:
         _exact(slots, "slots", (torch.int32,), (T, topk))
-    workspace, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
+    held, ws, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
     _call("qgemm_group_plan", dev, stream, T, topk, E, ids.data_ptr(), int(ids.dtype == torch.int64),
-          offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), workspace, ws_bytes)
+          offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), ws, ws_bytes)
+    del held
     return offsets, rows, slots
 
 
@@ -681,9 +686,10 @@ def qgemm_run_grouped(K: int, N: int, E: int, fmt, A, rows, offsets, Bq, scales,
                    ACTIVATIONS[activation] if isinstance(activation, str) else int(activation),
                    OUT_TYPES[out_type] if isinstance(out_type, str) else int(out_type))
     need = qgemm_grouped_workspace_size(S, a_rows, K, N, E, f)
-    workspace, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
+    held, ws, ws_bytes = _own_scratch(need, workspace, ws_bytes, dev, stream)
     _call("qgemm_run_grouped", dev, stream, S, a_rows, K, N, E, f, A.data_ptr(), _dev_ptr(rows), offsets.data_ptr(),
-          Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi), workspace, ws_bytes)
+          Bq.data_ptr(), scales.data_ptr(), C.data_ptr(), ctypes.byref(epi), ws, ws_bytes)
+    del held
 
 
 def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
