@@ -395,3 +395,48 @@ def test_split_k(M, K, N):
     err = (H.double() - full).abs()
     assert bool((err <= bound + (K + 16) * 2.0 ** -23 * (bias.abs().double() + res.abs().double())
                  + 2.0 ** -11 * full + 2.0 ** -25).all())
+
+
+# pre-activations at SiLU's corners: either side of where its exponential or
+# its reciprocal leave fp32's normal numbers, far beyond, and not numbers at all
+SILU_AT = np.array([-np.inf, -3.4e38, -1e30, -1e6, -300, -104, -100, -90, -88.8, -88.6, -87.5, -87.2, -80, -20, -1, -1e-3,
+                    -1e-38, -0.0, 0.0, 1e-38, 1e-3, 0.5, 3, 20, 80, 88, 90, 104, 300, 1e6, 1e30, 3.4e38, np.inf, np.nan],
+                   np.float32)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 64, 300), (7, 512, 68), (20, 128, 257), (40, 1024, 320), (300, 512, 520),
+                                   (12, 6144, 100), (200, 16448, 640)])
+@pytest.mark.parametrize("out", ["f32", "f16"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_silu_over_the_whole_range(fmt, M, K, N, out):
+    """x / (1 + e^-x) for every x, by the decode, tile, split-K and grouped
+    kernels (zero activations, so that the bias is x). An error of at most 4
+    units: one each of the hardware's exponential and reciprocal, half each of
+    three roundings, and the exponent's own; with an fp16 result |x| 2^-24 more
+    (the exponent rounded once) and its own half step. Results of less than
+    1.2e-36 may be zero. -infinity and NaN give NaN as the formula does."""
+    x = np.resize(SILU_AT, N)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    A = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, *Q.qgemm_mx_quantize_device(
+        torch.randn((N, K), device="cuda", generator=g)))
+    dt = torch.float16 if out == "f16" else torch.float32
+    C, D = torch.full((M, N), 7.0, dtype=dt, device="cuda"), torch.full((M, N), 7.0, dtype=dt, device="cuda")
+    Q.qgemm_run_ex(M, K, N, fmt, A, Bq, Sp, C, bias=dev(x), activation="silu", out_type=out)
+    Q.qgemm_run_grouped(K, N, 1, fmt, A, None, torch.tensor([0, M], dtype=torch.int32, device="cuda"), Bq, Sp, D,
+                        bias=dev(x[None]), activation="silu", out_type=out)
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = x.astype(np.float64) / (1.0 + np.exp(-x.astype(np.float64)))
+        ref = np.where(np.isneginf(x), np.nan, ref)
+        want = ref.astype(np.float16 if out == "f16" else np.float32)
+    num = np.isfinite(want)
+    tol = 4 * 2.0 ** -23 * np.abs(ref[num]) + 1.2e-36
+    if out == "f16":
+        tol = tol + np.minimum(np.abs(x[num].astype(np.float64)), 128) * 2.0 ** -23 * np.abs(ref[num]) \
+            + 2.0 ** -11 * np.abs(ref[num]) + 2.0 ** -25
+    for got in (C.cpu().numpy(), D.cpu().numpy()):
+        assert (np.isnan(got) == np.isnan(want)).all(), x[(np.isnan(got) != np.isnan(want)).any(0)]
+        inf = np.isinf(want)
+        assert (got[:, inf] == want[inf]).all(), x[inf]
+        err = np.abs(got[:, num].astype(np.float64) - ref[num])
+        assert (err <= tol).all(), (x[num][(err > tol).any(0)], got[:, num][0][(err > tol).any(0)])

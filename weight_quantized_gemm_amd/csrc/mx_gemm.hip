@@ -88,7 +88,10 @@ __device__ __forceinline__ void wave_lds_sync() {
 // e^-x = 2^t (1 + c) with t = -x log2 e in one rounding and c its error times
 // ln 2 (two fused multiply-adds, log2 e in two parts), so the hardware's
 // 2^t and 1 / d leave about two units. x is limited to [-88.5, 100] in the
-// exponent, where the result is x or below 1e-36 in size.
+// exponent: above, the result is x itself; below about -87.3 the reciprocal is
+// a subnormal number, which the hardware returns as zero, so the result is -0
+// however far x lies out (its value is less than 1.2e-36 in size), and NaN at
+// -infinity as from the division.
 // For an fp16 result the first rounding alone (a few 2^-24 of the value) is
 // far below the result's own.
 __device__ __forceinline__ float silu16(float v) {
