@@ -518,7 +518,9 @@ qgemm_status qgemm_group_plan(int T, int topk, int E, const void *ids, int ids64
  *             [S][N] in C's type (it may be C itself).
  * workspace: as qgemm_run_ex, of qgemm_grouped_workspace_size() bytes. No
  * host synchronisation: the sizes of the groups stay on the GPU.
- * Errors: ERR_FORMAT (any other format), ERR_SHAPE, ERR_NULL, ERR_ALIGN,
+ * Errors: ERR_FORMAT (any other format), ERR_SHAPE (also where S, E and N
+ * make tiles of 2^32 threads or more, the limit of a launch: from 1024
+ * experts of one row each over 2^20 columns on), ERR_NULL, ERR_ALIGN,
  * ERR_SIZE, ERR_DEVICE, ERR_NOMEM, ERR_LAUNCH. S, N or a_rows 0 is a no-op
  * (no rows to read means no slot).
  */

@@ -509,3 +509,27 @@ def test_two_threads_on_one_stream(fmt):
     for w, runs in zip(want, got):
         assert len(runs) == 40
         assert all(torch.equal(a, b) for r in runs for a, b in zip(w, r))
+
+
+def test_nearly_the_most_threads_of_a_launch():
+    """1024 experts of one row each over 2^20 - 128 columns: 512 threads short of
+    2^32 by one column of tiles, byte offsets of the weights and of C far past
+    32 bits. The experts share codes and differ in scale."""
+    E, K, N = 1024, 64, (1 << 20) - 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randint(0, 256, (N, K // 2), device="cuda", generator=g, dtype=torch.uint8)
+    s = torch.full((N, K // 32), 120, device="cuda", dtype=torch.uint8)
+    w = Q.qgemm_mx_dequantize_device(q, s).double()
+    wp, sp = Q.qgemm_mx_pack_device(K, N, q, s)
+    Bq = wp.expand(E, -1).contiguous().view(-1)
+    up = (torch.arange(E, device="cuda") % 8).to(torch.uint8)
+    Sp = torch.where(sp > 0, sp[None] + up[:, None], 0).to(torch.uint8).view(-1)
+    A = torch.randn((E, K), device="cuda", generator=g).half()
+    C = torch.full((E, N), float("nan"), dtype=torch.float16, device="cuda")
+    Q.qgemm_run_grouped(K, N, E, "mxfp4", A, None, torch.arange(E + 1, device="cuda", dtype=torch.int32), Bq, Sp, C,
+                        out_type="f16")
+    for e in range(0, E, 64):
+        a = A[e:e + 64].double() * 2.0 ** up[e:e + 64, None].double()
+        ref, mass = a @ w.t(), a.abs() @ w.abs().t()
+        err = (C[e:e + 64].double() - ref).abs()
+        assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 2.0 ** -11 * ref.abs() + 2.0 ** -25).all()), e

@@ -288,3 +288,27 @@ def test_scratch_lives_until_the_call_returns(call, monkeypatch):
                             torch.zeros(E + 1, dtype=torch.int32), torch.zeros(E * wb, dtype=torch.uint8),
                             torch.zeros(E * sb, dtype=torch.uint8), torch.zeros((S, N)))
     assert len(seen) == 1
+
+
+def test_a_launch_that_cannot_exist_is_refused_before_anything_is_enqueued():
+    """A launch has fewer than 2^32 threads along an axis. 1024 experts of one row
+    each: 2^20 columns make 2^13 x 2^10 tiles of 512 threads with fp16
+    activations, 2^22 columns 2^14 x 2^10 tiles of 256 with MXFP4 ones."""
+    lib = Q.load()
+    n = ctypes.c_size_t
+
+    def both(S, K, N, E, fmt):
+        size = lib.qgemm_grouped_workspace_size(S, S, K, N, E, fmt, ctypes.byref(ctypes.c_size_t()))
+        return size, lib.qgemm_run_grouped(S, S, K, N, E, fmt, A, None, A, A, A, A, None, None, n(0), None)
+
+    assert both(1024, 64, 1 << 20, 1024, 6) == (SHAPE, SHAPE)
+    assert both(1024, 64, (1 << 20) - 128, 1024, 6) == (OK, DEV)
+    assert both(1024, 64, 1 << 22, 1024, 8) == (SHAPE, SHAPE)
+    assert both(1024, 64, (1 << 22) - 256, 1024, 8) == (OK, DEV)
+    assert both(1 << 26, 64, 1 << 24, 1024, 8) == (SHAPE, SHAPE)
+    # ordinary large calls are not
+    for fmt in (6, 8):
+        assert both(1 << 20, 4096, 16384, 256, fmt) == (OK, DEV)
+        run = lambda M, K, N: lib.qgemm_run(M, K, N, fmt, A, A, A, A, None)
+        assert run(1 << 18, 4096, 1 << 17) == DEV and run(8, 64, 1 << 24) == DEV and run(40, 64, 1 << 24) == DEV
+        assert run(1 << 24, 64, 1 << 24) == SHAPE

@@ -65,7 +65,7 @@ static qgemm_status check_run(int M, int K, int N, qgemm_format f, const void *A
     if (M < 0 || M > (1 << 24)) return QGEMM_ERR_SHAPE;
     *empty = (M == 0 || N == 0);
     if (*empty) return QGEMM_OK;
-    if (is_mx(f) && mx_grid(M, 1, N) > 0x7FFFFFFFLL) return QGEMM_ERR_SHAPE;
+    if (is_mx(f) && !mx_launch_fits(f == QGEMM_MXFP4_A4, false, M, 1, K, N)) return QGEMM_ERR_SHAPE;
     if (!C) return QGEMM_ERR_NULL;
     if (K > 0 && (!A || !Bq)) return QGEMM_ERR_NULL;
     if (f == QGEMM_F32 || f == QGEMM_F16) {   // float weights: no pairs
@@ -517,7 +517,8 @@ static qgemm_status check_grouped(int S, int a_rows, int K, int N, int E, qgemm_
     if (st != QGEMM_OK) return st;
     if (S < 0 || S > (1 << 26) || a_rows < 0 || a_rows > (1 << 26) || E < 1 || E > QGEMM_MAX_EXPERTS)
         return QGEMM_ERR_SHAPE;
-    return mx_grid(S, E, N) > 0x7FFFFFFFLL ? QGEMM_ERR_SHAPE : QGEMM_OK;
+    if (S == 0 || N == 0) return QGEMM_OK;
+    return mx_launch_fits(f == QGEMM_MXFP4_A4, true, S, E, K, N) ? QGEMM_OK : QGEMM_ERR_SHAPE;
 }
 
 qgemm_status qgemm_grouped_workspace_size(int S, int a_rows, int K, int N, int E, qgemm_format f, size_t *bytes) {

@@ -133,9 +133,10 @@ MxWorkspace mx_workspace(qgemm_format f, long long rows, int K) {
     return w;
 }
 
-long long mx_grid(int S, int E, int N) {
+// The most row tiles of `rows` rows that S slots in E groups can make.
+long long mx_row_tiles(int S, int E, int rows) {
     const long long groups = E < S ? E : S;
-    return (groups + (S - groups) / 8) * div_up(N, 32) + 7;
+    return groups + (S - groups) / rows;
 }
 
 // All rows in whole tiles, and half a tile more for every group that has rows
@@ -193,6 +194,35 @@ MxPlan mx_dense_plan(bool A4, int M, int K, int N) {
         }
     }
     return best;
+}
+
+// The grouped product's tile (measurements beside the kernels).
+MxShape mx_grouped_shape(bool A4, int S, int E, int N) {
+    auto tiles = [&](MxShape t) { return mx_expect_tiles(t, S, E, N); };
+    const int rows = S / (S < E ? S : E);      // of the average group
+    if (A4 && rows >= 128 && tiles(T128x256) >= kMxEnoughTiles) return T128x256;
+    if (rows >= 24 && tiles(T64x256) >= kMxEnoughTiles) return T64x256;
+    if (rows >= 24 && tiles(T64x128) >= kMxEnoughTiles) return T64x128;
+    if (rows >= (A4 ? 1 : 6) && tiles(T32x256) >= kSplitTargetCUs) return T32x256;
+    if (tiles(T32x128) >= kMxEnoughTiles) return T32x128;
+    return tiles(T32x64) >= kMxEnoughTiles ? T32x64 : T32x32;
+}
+
+// Few rows a group and too few 32 x 128 tiles to fill the CUs.
+bool mx_grouped_decode(int S, int E, int N) {
+    return S / (S < E ? S : E) <= 2 && mx_expect_tiles(T32x128, S, E, N) < kMxEnoughTiles;
+}
+
+// 1024 experts of a row each over 2^20 columns are 2^23 tiles of 32 x 128 with
+// 512 threads: such a launch does not exist.
+bool mx_launch_fits(bool A4, bool grouped, int S, int E, int K, int N) {
+    constexpr long long most = 0xFFFFFFFFLL;
+    // no kernel has more than 1024 threads for 8 x 32 outputs (the one for few
+    // rows always ends here: it takes at most 8 rows, or few tiles)
+    if ((mx_row_tiles(S, E, 8) * div_up(N, 32) + 7) * 1024 <= most) return true;
+    const MxShape t = grouped ? mx_grouped_shape(A4, S, E, N) : mx_dense_plan(A4, S, K, N).shape;
+    const long long grid = (mx_row_tiles(S, E, kMxTileRows[t]) * div_up(N, kMxTileCols[t]) + 7) / 8 * 8;
+    return grid * kMxTileThreads[A4][t] <= most;
 }
 
 int f32_kgroups(int M, int N) {

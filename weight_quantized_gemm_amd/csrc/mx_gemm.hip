@@ -706,6 +706,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void mx_decode_kernel(MxArgs p) 
 }  // namespace
 
 namespace {
+
 // ---------------------------------------------------------------------------
 // Which kernel runs. Large tiles move fewer bytes into a CU for each matrix
 // instruction; small ones, and more K groups in a workgroup, keep 256 CUs busy
@@ -749,27 +750,13 @@ namespace {
 // Split K (dense, few tiles) multiplies the workgroups by the slices of K; a
 // second launch adds the slices up in their order and applies the epilogue.
 // ---------------------------------------------------------------------------
-MxShape grouped_shape(bool A4, int S, int E, int N) {
-    auto tiles = [&](MxShape t) { return mx_expect_tiles(t, S, E, N); };
-    const int rows = S / (S < E ? S : E);      // of the average group
-    if (A4 && rows >= 128 && tiles(T128x256) >= kMxEnoughTiles) return T128x256;
-    if (rows >= 24 && tiles(T64x256) >= kMxEnoughTiles) return T64x256;
-    if (rows >= 24 && tiles(T64x128) >= kMxEnoughTiles) return T64x128;
-    if (rows >= (A4 ? 1 : 6) && tiles(T32x256) >= kSplitTargetCUs) return T32x256;
-    if (tiles(T32x128) >= kMxEnoughTiles) return T32x128;
-    return tiles(T32x64) >= kMxEnoughTiles ? T32x64 : T32x32;
-}
-
-// The most row tiles of `rows` rows that S slots in E groups can make.
-long long most_row_tiles(int S, int E, int rows) {
-    const long long groups = E < S ? E : S;
-    return groups + (S - groups) / rows;
-}
-
-template <class T>
+template <MxShape SHAPE, class T>
 hipError_t launch_tile(MxArgs p, hipStream_t s) {
+    static_assert(T::BM == kMxTileRows[SHAPE] && T::BN == kMxTileCols[SHAPE] &&
+                      T::THREADS == kMxTileThreads[T::A4][SHAPE],
+                  "the shape the host counts with");
     p.tiles_n = div_up(p.N, T::BN);
-    const long long grid = most_row_tiles(p.S, p.offsets ? p.E : 1, T::BM) * p.tiles_n;
+    const long long grid = mx_row_tiles(p.S, p.offsets ? p.E : 1, T::BM) * p.tiles_n;
     hipLaunchKernelGGL(mx_tile_kernel<T>, dim3((unsigned)((grid + 7) / 8 * 8), (unsigned)p.nsplit), dim3(T::THREADS), 0,
                        s, p);
     return hipGetLastError();
@@ -778,7 +765,7 @@ hipError_t launch_tile(MxArgs p, hipStream_t s) {
 template <bool A4, int RT, bool ONCE>
 hipError_t launch_decode_rows(MxArgs p, hipStream_t s) {
     p.tiles_n = div_up(p.N, 32);
-    const long long grid = most_row_tiles(p.S, p.offsets ? p.E : 1, RT) * p.tiles_n;
+    const long long grid = mx_row_tiles(p.S, p.offsets ? p.E : 1, RT) * p.tiles_n;
     hipLaunchKernelGGL((mx_decode_kernel<A4, RT, ONCE>), dim3((unsigned)((grid + 7) / 8 * 8)),
                        dim3(64 * kDecodeWaves), 0, s, p);
     return hipGetLastError();
@@ -796,13 +783,13 @@ template <bool A4>
 hipError_t launch_shape(MxShape shape, const MxArgs &p, hipStream_t s) {
     switch (shape) {
     //                                       RF CF WM WN WK NS BR waves a SIMD
-    case T128x256: return launch_tile<Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
-    case T64x256:  return launch_tile<Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
-    case T64x128:  return launch_tile<Tile<A4, 2, 1, 1, 4, A4 ? 2 : 4, 4, 2, A4 ? 2 : 4>>(p, s);
-    case T32x256:  return launch_tile<Tile<A4, 1, 2, 1, 4, 1, 4, 2, 2>>(p, s);
-    case T32x128:  return launch_tile<Tile<A4, 1, 1, 1, 4, 2, 4, 2, 2>>(p, s);
-    case T32x64:   return launch_tile<Tile<A4, 1, 1, 1, 2, 4, 4, 2, 2>>(p, s);
-    default:       return launch_tile<Tile<A4, 1, 1, 1, 1, 8, 4, 2, 1>>(p, s);
+    case T128x256: return launch_tile<T128x256, Tile<A4, 4, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T64x256:  return launch_tile<T64x256, Tile<A4, 2, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T64x128:  return launch_tile<T64x128, Tile<A4, 2, 1, 1, 4, A4 ? 2 : 4, 4, 2, A4 ? 2 : 4>>(p, s);
+    case T32x256:  return launch_tile<T32x256, Tile<A4, 1, 2, 1, 4, 1, 4, 2, 2>>(p, s);
+    case T32x128:  return launch_tile<T32x128, Tile<A4, 1, 1, 1, 4, 2, 4, 2, 2>>(p, s);
+    case T32x64:   return launch_tile<T32x64, Tile<A4, 1, 1, 1, 2, 4, 4, 2, 2>>(p, s);
+    default:       return launch_tile<T32x32, Tile<A4, 1, 1, 1, 1, 8, 4, 2, 1>>(p, s);
     }
 }
 
@@ -815,17 +802,12 @@ hipError_t launch_tiles(const MxArgs &args, hipStream_t s) {
         const hipError_t e = launch_shape<A4>(mx_dense_plan(A4, p.S, p.K, p.N).shape, p, s);
         return e != hipSuccess ? e : launch_splitk_reduce_f32(args.part, args.nsplit, p.S, p.N, args.C, args.epi, s);
     }
-    return launch_shape<A4>(args.offsets ? grouped_shape(A4, args.S, args.E, args.N)
+    return launch_shape<A4>(args.offsets ? mx_grouped_shape(A4, args.S, args.E, args.N)
                                          : mx_dense_plan(A4, args.S, args.K, args.N).shape,
                             args, s);
 }
 
 }  // namespace
-
-// Few rows a group and too few 32 x 128 tiles to fill the CUs.
-bool mx_grouped_decode(int S, int E, int N) {
-    return S / (S < E ? S : E) <= 2 && mx_expect_tiles(T32x128, S, E, N) < kMxEnoughTiles;
-}
 
 hipError_t launch_mx_gemm(qgemm_format f, const MxArgs &args, bool decode, void *ws, hipStream_t s) {
     MxArgs p = args;

@@ -310,12 +310,14 @@ struct MxWorkspace {
     size_t q_off, s_off, bytes;
 };
 MxWorkspace mx_workspace(qgemm_format f, long long rows, int K);
-// Workgroups of the product's launch, at most (2^31 - 1 are allowed).
-long long mx_grid(int S, int E, int N);
+// The most row tiles of `rows` rows that S slots in E groups can make.
+long long mx_row_tiles(int S, int E, int rows);
 // Tiles of the tiled product (rows x columns).
 enum MxShape { T128x256, T64x256, T64x128, T32x256, T32x128, T32x64, T32x32 };
 constexpr int kMxEnoughTiles = 144;     // of 256 CUs: from here a larger tile beats more workgroups
 constexpr int kMxTileRows[] = {128, 64, 64, 32, 32, 32, 32}, kMxTileCols[] = {256, 256, 128, 256, 128, 64, 32};
+// Threads of a workgroup, with fp16 and with MXFP4 activations.
+constexpr int kMxTileThreads[2][7] = {{256, 256, 1024, 256, 512, 512, 512}, {256, 256, 512, 256, 512, 512, 512}};
 // Tiles to expect of S slots in E groups.
 long long mx_expect_tiles(MxShape t, int S, int E, int N);
 // The dense product's tile, and slices of K; a function of the shape alone.
@@ -324,6 +326,10 @@ struct MxPlan {
     int nsplit;
 };
 MxPlan mx_dense_plan(bool A4, int M, int K, int N);
+// The grouped product's.
+MxShape mx_grouped_shape(bool A4, int S, int E, int N);
+// Whether the product's launch has fewer than 2^32 threads along x, as it must.
+bool mx_launch_fits(bool A4, bool grouped, int S, int E, int K, int N);
 // decode: the kernel for few rows, which needs no scratch; for the dense product
 // up to the GEMV limit's rows, for a grouped one as mx_grouped_decode says.
 bool mx_grouped_decode(int S, int E, int N);
