@@ -533,3 +533,77 @@ def test_nearly_the_most_threads_of_a_launch():
         ref, mass = a @ w.t(), a.abs() @ w.abs().t()
         err = (C[e:e + 64].double() - ref).abs()
         assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 2.0 ** -11 * ref.abs() + 2.0 ** -25).all()), e
+
+
+# average rows, experts and columns that reach the tiles between the smallest
+# and the largest: 32 x 256 (four-column epilogue and an odd width), 64 x 128, 32 x
+# 64, 32 x 32 and 64 x 256 (tests/test_mx_tiles.py checks what they reach)
+MIDDLE = [(8, 12, 8200), (8, 12, 8203), (2, 12, 8200), (13, 13, 8200), (40, 12, 2500), (14, 12, 1300), (20, 5, 300),
+          (40, 12, 8200)]
+# one, two, three and no stages more than whole turns of four, of 64 elements (fp16 activations) and of 256
+MIDDLE_K = [64, 128, 192, 256, 448, 640, 832, 1088, 1280]
+
+
+def middle_sizes(mean, E, K):
+    """Rows of each expert: none to twice the average, the last one empty."""
+    sizes = np.random.default_rng(mean + K).integers(0, 2 * mean + 1, E)
+    sizes[0], sizes[E - 1] = 2 * mean, 0
+    return sizes
+
+
+def _middle(fmt, mean, E, N, K):
+    """(A, rows, offsets, Bq, scales, C, [float64 values of A's rows], [of the weights])."""
+    offsets = np.concatenate([[0], np.cumsum(middle_sizes(mean, E, K))]).astype(np.int32)
+    n = int(offsets[-1])
+    T, S = max(3, n // 3), n + 7
+    g = torch.Generator(device="cuda").manual_seed(mean + K)
+    A = torch.randn((T, K), device="cuda", generator=g).half()
+    rows = torch.randint(0, T, (S,), device="cuda", generator=g, dtype=torch.int32)
+    q, s = Q.qgemm_mx_quantize_device(torch.randn((E * N, K), device="cuda", generator=g))
+    w = Q.qgemm_mx_dequantize_device(q, s).view(E, N, K)
+    a = Q.qgemm_mx_dequantize_device(*Q.qgemm_mx_quantize_device(A)).double() if fmt == "mxfp4a4" else A.double()
+    return A, rows, offsets, *Q.qgemm_mx_pack_device(K, N, q, s, E=E), a, w
+
+
+@pytest.mark.parametrize("K", MIDDLE_K)
+@pytest.mark.parametrize("mean,E,N", MIDDLE)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_middle_tiles_of_the_grouped_product(fmt, mean, E, N, K):
+    """Ragged groups, rows gathered, K of every number of stages left over, rows
+    behind the last group untouched; bounds as in check_product."""
+    A, rows, offsets, Bq, Sp, a, w = _middle(fmt, mean, E, N, K)
+    n, S = int(offsets[-1]), rows.numel()
+    C = torch.full((S, N), 9.0, device="cuda")
+    Q.qgemm_run_grouped(K, N, E, fmt, A, rows, dev(offsets), Bq, Sp, C)
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        x, we = a[rows[lo:hi].long()], w[e].double()
+        ref, mass = x @ we.t(), x.abs() @ we.abs().t()
+        err = (C[lo:hi].double() - ref).abs()
+        assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 1e-37).all()), e
+        assert float(err.norm()) <= 4 * (K + 16) ** 0.5 * 2.0 ** -24 * float(mass.norm()), e
+    assert bool((C[n:] == 9.0).all())
+
+
+@pytest.mark.parametrize("mean,E,N", MIDDLE)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_middle_tiles_with_an_epilogue(fmt, mean, E, N):
+    """Slot s reads row s, bias of the row's own expert, residual in place, ReLU
+    (slope 1), fp16 result (half a step more)."""
+    K = 576
+    A, rows, offsets, Bq, Sp, a, w = _middle(fmt, mean, E, N, K)
+    n, S = int(offsets[-1]), rows.numel()
+    A, a = A[rows.long()].contiguous(), a[rows.long()]
+    g = torch.Generator(device="cuda").manual_seed(N)
+    bias, res = torch.randn((E, N), device="cuda", generator=g), torch.randn((S, N), device="cuda", generator=g).half()
+    C = res.clone()
+    Q.qgemm_run_grouped(K, N, E, fmt, A, None, dev(offsets), Bq, Sp, C, bias=bias, residual=C, activation="relu",
+                        out_type="f16")
+    for e in range(E):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        we, b, r = w[e].double(), bias[e].double(), res[at].double()
+        ref = (a[at] @ we.t() + b + r).clamp(min=0)
+        mass = a[at].abs() @ we.abs().t() + b.abs() + r.abs()
+        err = (C[at].double() - ref).abs()
+        assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 2.0 ** -11 * ref + 2.0 ** -25).all()), e
+    assert torch.equal(C[n:], res[n:])

@@ -440,3 +440,18 @@ def test_silu_over_the_whole_range(fmt, M, K, N, out):
         assert (got[:, inf] == want[inf]).all(), x[inf]
         err = np.abs(got[:, num].astype(np.float64) - ref[num])
         assert (err <= tol).all(), (x[num][(err > tol).any(0)], got[:, num][0][(err > tol).any(0)])
+
+
+# (M, N) that reach 32 x 128, 64 x 128, 64 x 256 and 128 x 256 tiles with fp16
+# activations whatever K, and K of one, two, three and no stages more than whole
+# turns of four, of 64 elements (fp16 activations) and of 256
+# (tests/test_mx_tiles.py checks both)
+MIDDLE = [(200, 4100), (500, 3620), (250, 16300), (1000, 16300)]
+MIDDLE_K = [64, 128, 192, 256, 448, 640, 832, 1088, 1280]
+
+
+@pytest.mark.parametrize("K", MIDDLE_K)
+@pytest.mark.parametrize("M,N", MIDDLE)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_middle_tiles_with_stages_left_over(fmt, M, N, K):
+    test_every_tile_with_stages_left_over(fmt, M, N, K)
