@@ -607,3 +607,61 @@ def test_middle_tiles_with_an_epilogue(fmt, mean, E, N):
         err = (C[at].double() - ref).abs()
         assert bool((err <= (K + 16) * 2.0 ** -23 * mass + 2.0 ** -11 * ref + 2.0 ** -25).all()), e
     assert torch.equal(C[n:], res[n:])
+
+
+@pytest.mark.parametrize("T,topk,E", [(150000, 8, 128), (1048577, 1, 1024), (1 << 23, 8, 7)])
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_plan_of_millions_of_choices(T, topk, E, drop):
+    """More than 2^20 choices, up to the most there may be (2^26)."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    ids = torch.randint(0, E, (T, topk), device="cuda", generator=g, dtype=torch.int32)
+    ids = torch.where(torch.rand((T, topk), device="cuda", generator=g) < drop, -1 - ids, ids)
+    offsets, rows, slots = Q.qgemm_group_plan(ids, E)
+    key = torch.where(ids < 0, E, ids).view(-1)
+    by_key, order = torch.sort(key, stable=True)
+    assert torch.equal(offsets, torch.searchsorted(by_key, torch.arange(E + 1, device="cuda",
+                                                                        dtype=torch.int32)).to(torch.int32))
+    assert torch.equal(rows, (order // topk).to(torch.int32))
+    place = torch.empty_like(order)
+    place[order] = torch.arange(order.numel(), device="cuda")
+    assert torch.equal(slots.view(-1), torch.where(key < E, place, -1).to(torch.int32))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+@pytest.mark.parametrize("at", [0, 77, 127])
+def test_all_rows_of_many_experts_at_one(fmt, at):
+    """As many slots as a quarter of the experts, for which two-row tiles are
+    planned, and every one of them the same expert's."""
+    E, K, N, S = 128, 576, 100, 32
+    rng = np.random.default_rng(at)
+    ex = Experts(fmt, E, K, N, 7)
+    A = _acts(rng, S, K)
+    offsets = np.where(np.arange(E + 1) > at, S, 0).astype(np.int32)
+    ref, sumabs = ex.reference(A, np.arange(S), offsets)
+    C = torch.full((S, N), 9.0, device="cuda")
+    ex.run(dev(A), None, dev(offsets), C)
+    X.check_product(C.cpu().numpy(), ref, sumabs, K, what=f"{fmt} {at}")
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_activations_past_four_gigabytes(fmt, grouped):
+    """Rows read in order: A (17 GB) and its codes (4.3 GB) far past 32-bit byte
+    offsets, dense and as two groups that meet inside a tile."""
+    M, K, N = (1 << 19) + 5, 16384, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = torch.randn((M, K), device="cuda", generator=g, dtype=torch.float16)
+    q, s = Q.qgemm_mx_quantize_device(torch.randn((2 * N, K), device="cuda", generator=g))
+    w = Q.qgemm_mx_dequantize_device(q, s).view(2, N, K).double()
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, q, s, E=2)
+    C = torch.full((M, N), float("nan"), device="cuda")
+    cut = M - 41
+    if grouped:
+        Q.qgemm_run_grouped(K, N, 2, fmt, A, None, torch.tensor([0, cut, M], device="cuda", dtype=torch.int32), Bq, Sp, C)
+    else:
+        Q.qgemm_run_ex(M, K, N, fmt, A, Bq, Sp, C)
+    for lo, hi in ((0, 130), (131000, 131200), (262100, 262200), (M - 200, cut), (cut, M)):
+        a = Q.qgemm_mx_dequantize_device(*Q.qgemm_mx_quantize_device(A[lo:hi])) if fmt == "mxfp4a4" else A[lo:hi]
+        a, we = a.double(), w[1 if grouped and lo >= cut else 0]
+        err = (C[lo:hi].double() - a @ we.t()).abs()
+        assert bool((err <= (K + 16) * 2.0 ** -23 * (a.abs() @ we.abs().t()) + 1e-37).all()), lo
