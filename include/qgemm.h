@@ -488,8 +488,8 @@ qgemm_status qgemm_mx_pack_device(int K, int N, int E, const uint8_t *q, const u
  *   slots    device int32 [T][topk]: the slot of a choice, -1 without one.
  * All outputs are fully written (T == 0 or topk == 0: offsets, all zero).
  * workspace: device scratch of qgemm_group_plan_size() bytes, 16-byte aligned;
- * with NULL and 0 any that is needed is allocated stream-ordered. Calls that
- * share one must be ordered. Deterministic.
+ * with NULL and 0 any that is needed is allocated stream-ordered (give one under
+ * graph capture). Calls that share one must be ordered. Deterministic.
  * Errors: ERR_SHAPE (E outside 1..QGEMM_MAX_EXPERTS, T * topk above 2^26, a
  * negative size), ERR_NULL, ERR_ALIGN, ERR_SIZE, ERR_DEVICE, ERR_NOMEM,
  * ERR_LAUNCH.
@@ -516,8 +516,9 @@ qgemm_status qgemm_group_plan(int T, int topk, int E, const void *ids, int ids64
  *   C         device, float or fp16 [S][N] per the epilogue.
  *   epilogue  NULL, or as qgemm_run_ex with bias float [E][N] and residual
  *             [S][N] in C's type (it may be C itself).
- * workspace: as qgemm_run_ex, of qgemm_grouped_workspace_size() bytes. No
- * host synchronisation: the sizes of the groups stay on the GPU.
+ * workspace: as qgemm_run_ex, of qgemm_grouped_workspace_size() bytes (give one
+ * under graph capture). No host synchronisation: the sizes of the groups stay
+ * on the GPU.
  * Errors: ERR_FORMAT (any other format), ERR_SHAPE (also where S, E and N
  * make tiles of 2^32 threads or more, the limit of a launch: from 1024
  * experts of one row each over 2^20 columns on), ERR_NULL, ERR_ALIGN,

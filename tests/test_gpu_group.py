@@ -665,3 +665,44 @@ def test_activations_past_four_gigabytes(fmt, grouped):
         a, we = a.double(), w[1 if grouped and lo >= cut else 0]
         err = (C[lo:hi].double() - a @ we.t()).abs()
         assert bool((err <= (K + 16) * 2.0 ** -23 * (a.abs() @ we.abs().t()) + 1e-37).all()), lo
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp4a4"])
+def test_two_graphs_without_a_workspace(fmt):
+    """Two captured layers whose plan and products take their scratch from torch's
+    allocator (each graph's own pool), replayed in turn with new inputs and
+    eager calls of the same sizes between them."""
+    T, topk, E, K, N = 1500, 2, 6, 320, 192
+    g = torch.Generator(device="cuda").manual_seed(8)
+    Bq, Sp = Q.qgemm_mx_pack_device(K, N, *Q.qgemm_mx_quantize_device(
+        torch.randn((E * N, K), device="cuda", generator=g)), E=E)
+    assert Q.qgemm_group_plan_size(T, topk, E) > 0
+
+    def fresh():
+        return (torch.randint(0, E + 1, (T, topk), device="cuda", generator=g, dtype=torch.int32),
+                torch.randn((T, K), device="cuda", generator=g).half())
+
+    def layer(ids, A, C):
+        offsets, rows, slots = Q.qgemm_group_plan(ids, E)
+        C.zero_()
+        Q.qgemm_run_grouped(K, N, E, fmt, A, rows, offsets, Bq, Sp, C)
+        return slots
+
+    sets = []
+    for _ in range(2):
+        ids, A = fresh()
+        C = torch.empty((T * topk, N), device="cuda")
+        layer(ids, A, C)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            slots = layer(ids, A, C)
+        sets.append((graph, ids, A, C, slots))
+    for turn in range(6):
+        graph, ids, A, C, slots = sets[turn % 2]
+        for t, new in zip((ids, A), fresh()):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.empty_like(C)
+        assert torch.equal(layer(ids, A, want), slots) and torch.equal(C, want)
