@@ -38,7 +38,8 @@
  *                   32 K-elements; fp16 activations. K % 64 == 0. The product
  *                   takes the weights in fp16: exact for scales 2^-23 ..
  *                   2^13, rounded once below (to subnormals and zero), and
- *                   infinite above 65504.
+ *                   infinite above 65504 (NaN against a zero activation);
+ *                   QGEMM_MXFP4_A4 takes such weights as they are.
  *   QGEMM_MXFP4_A4  MXFP4 weights as above, and every row of A quantised to
  *                   MXFP4 on the fly: both operands enter the matrix cores as
  *                   4-bit codes with their scales, fp32 accumulation, for

@@ -239,8 +239,11 @@ hipError_t plan(int S, int topk, int E, const I *ids, int32_t *offsets, int32_t 
 // fp32 fused multiply-adds, one rounding. A thread owns VEC neighbouring
 // columns of one token: every row of Y is read once in whole vectors, C is
 // written once, and no atomics are needed. Bound by memory: 4099 tokens of 4
-// fp16 rows of 4096 columns (168 MB) 27 us, as fast as a large copy; 16 tokens
-// of 8 rows 3.6 us, of which most is the launch.
+// fp16 rows of 4096 columns (168 MB) 34 us from memory (4.9 TB/s; a tenth of
+// the choices elsewhere and two sets in turn, partly from the last-level cache,
+// 28); 16 tokens of 8 rows 3.8 us, of which most is the launch. Where N is not a
+// multiple of 8 a thread owns one column and the loads are what bounds it: 4100
+// columns 105 us, 1.6 TB/s.
 // Block x covers one of `cols` column strips of one of `per` tokens, block y
 // the next `per`: the threads of a launch along x must stay below 2^32.
 // ---------------------------------------------------------------------------

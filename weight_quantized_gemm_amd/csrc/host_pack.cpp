@@ -155,13 +155,14 @@ long long mx_expect_tiles(MxShape t, int S, int E, int N) {
 // Large tiles where they are enough (measurements beside the kernels), and
 // with MXFP4 activations the smaller ones likewise.
 //
-// With fp16 activations a workgroup of the smaller tiles is bound by the bytes
-// it brings into its CU: 2 a row and 17/32 a column of its tile for every
-// K-element. Where tiles are few and K is long, a split of K divides them over
+// With fp16 activations the time of a workgroup of the smaller tiles goes with
+// the bytes it brings into its CU: 2 a row and 17/32 a column of its tile for
+// every K-element (the unit that brings them in is the busiest, 63 % at 512 x
+// 4096 x 4096, but none is full). Where tiles are few and K is long, a split of K divides them over
 // the CUs that have no tile, and larger tiles, too few by themselves, need
 // fewer bytes for each output; it costs a second launch and the partial tiles,
 // written and read once. Estimated time (us): a round of tiles takes its bytes
-// at 75 GB/s and 4 bytes an output at 6.8 GB/s; a split 2.2 and its partial
+// at 75 GB/s (fitted, not a limit) and 4 bytes an output at 6.8 GB/s; a split 2.2 and its partial
 // tiles at 5.5 TB/s. Fitted to 43 shapes with M = 10 to 512: the choices are 1 %
 // above the best of all tiles and slices there on average, 17 % at most.
 // Measured, tile by count alone -> by estimate: 32 x 9728 x 2560 12.9 -> 10.8

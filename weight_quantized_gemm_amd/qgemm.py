@@ -714,7 +714,9 @@ def qgemm_group_combine(Y, slots, weights, C, stream=None) -> None:
 # ---------------------------------------------------------------------------
 class PackedWeight:
     """Quantise (or take) a weight, pack it and upload it to the GPU. For the
-    MXFP4 formats the pairs are the scale bytes [N][K/32]."""
+    MXFP4 formats the pairs are the scale bytes [N][K/32]; "mxfp4" products take
+    the weights in fp16 (exact for scales 2^-23 .. 2^13, infinite above 65504),
+    "mxfp4a4" ones as they are."""
 
     def __init__(self, fmt, K: int, N: int, w_canonical: np.ndarray,
                  pairs_canonical: np.ndarray | None, device="cuda"):
